@@ -25,7 +25,8 @@ LIB = os.path.join(HERE, "libqpn.so")
 SANITIZE_DIR = os.path.join(BUILD, "sanitize")
 SANITIZED_LIB = os.path.join(SANITIZE_DIR, "libqpn.so")
 
-SOURCES = ["qpn_api.cpp", "qpn_gemm.hip", "qpn_pack.hip", "qpn_prefill.hip"]
+SOURCES = ["qpn_api.cpp", "qpn_gemm.hip", "qpn_pack.hip", "qpn_prefill.hip",
+           "qpn_kv_api.cpp", "qpn_kv_round.hip", "qpn_kv_attn.hip", "qpn_kv_verify.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -10,6 +10,7 @@
 
 #include "qpn_common.h"
 #include "qpn_internal.h"
+#include "qpn_kv_internal.h"
 
 namespace {
 
@@ -62,6 +63,13 @@ int device_check() {
   });
   return g_ok[dev] ? QPN_OK : QPN_ERR_DEVICE;
 }
+
+}  // namespace
+
+// the same check for the other entry points of the library
+int qpn::device_status() { return device_check(); }
+
+namespace {
 
 int launch_status(hipError_t e) { return e == hipSuccess ? QPN_OK : QPN_ERR_LAUNCH; }
 

@@ -1,0 +1,541 @@
+// qpn_kv_round.hip -- what opens a speculative round and feeds the 8-bit paged
+// KV cache on gfx950: page tables and slots from the requests' lengths, and
+// the query/key norms with the rotation and the cache append.
+#include "qpn_common.h"
+#include "qpn_kv_internal.h"
+
+namespace qpn {
+
+namespace {
+
+// ---------------------------------------------------------------------------
+// Page tables, slots and positions of a round.
+//
+// One workgroup: two block scans over the requests (pages and rows asked for,
+// which decide admission; then those of the admitted requests, which place
+// them), kept in LDS, after which every new table entry and every row finds
+// its request by bisection.  The work is a few KiB at most, so the launch and
+// five dependent passes (loads, two scans, bisection, stores) are all there
+// is to pay.
+// ---------------------------------------------------------------------------
+constexpr int kPlanThreads = 1024;
+constexpr int kPlanWaves = kPlanThreads / kLanes;
+
+struct Pair64 {
+  int64_t a, b;
+};
+
+__device__ __forceinline__ Pair64 block_inclusive_scan(Pair64 x, Pair64* waves) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const int64_t a = __shfl_up(x.a, d), b = __shfl_up(x.b, d);
+    if (lane >= d) x.a += a, x.b += b;
+  }
+  __syncthreads();  // the previous scan's totals have been read
+  if (lane == 63) waves[wave] = x;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) x.a += waves[w].a, x.b += waves[w].b;
+  return x;
+}
+
+// The last index i in [0, n) with start[i] <= x (start ascending, start[0] <= x).
+__device__ __forceinline__ int bisect(const int32_t* start, int n, int32_t x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (start[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_round_kernel(PlanRoundArgs a) {
+  __shared__ int32_t s_row[kKvMaxRequests + 1];   // first row of each request
+  __shared__ int32_t s_take[kKvMaxRequests + 1];  // pages taken before each request
+  __shared__ Pair64 s_waves[kPlanWaves];
+  __shared__ Pair64 s_carry;
+  const int tid = threadIdx.x;
+  const int chunks = (a.requests + kPlanThreads - 1) / kPlanThreads;
+  int64_t free_count = *a.free_count;
+  free_count = free_count < 0 ? 0 : free_count > a.free_capacity ? a.free_capacity : free_count;
+
+  struct Asked {
+    bool fine;
+    int64_t before, rows, want;
+  };
+  auto asked_of = [&](int r) {
+    Asked q{false, 0, 0, 0};
+    if (r < a.requests) {
+      q.before = a.before[r];
+      q.rows = a.rows[r];
+      const int64_t held = a.held[r], need = (q.before + q.rows + kKvPage - 1) / kKvPage;
+      q.fine = q.before >= 0 && q.rows >= 0 && held >= 0 && held <= a.table_width &&
+               need <= a.table_width && q.before <= held * kKvPage;
+      q.want = q.fine && need > held ? need - held : 0;
+      if (!q.fine) q.rows = 0;
+    }
+    return q;
+  };
+
+  Pair64 asked_before{0, 0}, placed_before{0, 0};  // totals of the former chunks
+  for (int c = 0; c < chunks; ++c) {
+    const int r = c * kPlanThreads + tid;
+    const Asked q = asked_of(r);
+    Pair64 up = block_inclusive_scan({q.want, q.rows}, s_waves);
+    up.a += asked_before.a, up.b += asked_before.b;
+    const bool go = q.fine && up.a <= free_count && up.b <= a.capacity;
+    if (tid == kPlanThreads - 1) s_carry = up;
+    const Pair64 mine{go ? q.want : 0, go ? q.rows : 0};
+    Pair64 at = block_inclusive_scan(mine, s_waves);  // (its barriers publish s_carry)
+    asked_before = s_carry;
+    at.a += placed_before.a, at.b += placed_before.b;
+    if (r < a.requests) {
+      s_row[r] = (int32_t)(at.b - mine.b);
+      s_take[r] = (int32_t)(at.a - mine.a);
+      a.row_start[r] = (int32_t)(at.b - mine.b);
+      a.seq_lens[r] = q.fine ? (int32_t)(q.before + mine.b) : 0;
+    }
+    __syncthreads();  // s_carry has been read
+    if (tid == kPlanThreads - 1) s_carry = at;
+    __syncthreads();
+    placed_before = s_carry;
+    __syncthreads();
+  }
+  const int32_t pages = (int32_t)placed_before.a, rows = (int32_t)placed_before.b;
+  if (tid == 0) {
+    s_row[a.requests] = rows;
+    s_take[a.requests] = pages;
+    a.row_start[a.requests] = rows;
+  }
+  __syncthreads();
+
+  // the entry `index` of request r's table row, new pages from the free list
+  auto page_of = [&](int r, int64_t held, int64_t index) {
+    return index < held ? a.table[r * a.table_stride + index]
+                        : a.free_pages[free_count - 1 - (s_take[r] + (index - held))];
+  };
+  for (int k = tid; k < pages; k += kPlanThreads) {
+    const int r = bisect(s_take, a.requests, k);
+    a.table[r * a.table_stride + a.held[r] + (k - s_take[r])] = a.free_pages[free_count - 1 - k];
+  }
+  for (int t = tid; t < a.capacity; t += kPlanThreads) {
+    int32_t slot = -1, position = 0;
+    if (t < rows) {
+      const int r = bisect(s_row, a.requests, t);
+      position = a.before[r] + (t - s_row[r]);
+      const int32_t page = page_of(r, a.held[r], position / kKvPage);
+      if (page >= 0 && page <= kKvMaxPages) slot = page * kKvPage + position % kKvPage;
+    }
+    a.slots[t] = slot;
+    a.positions[t] = position;
+  }
+  __syncthreads();  // held has been read (held_out may be held)
+  for (int r = tid; r < a.requests; r += kPlanThreads)
+    a.held_out[r] = a.held[r] + (s_take[r + 1] - s_take[r]);
+  if (tid == 0) *a.free_count_out = (int32_t)(free_count - pages);
+}
+
+// ---------------------------------------------------------------------------
+// Norms, rotation and cache append.
+//
+// A head of DIM dimensions lies over LPH = DIM / 8 neighbouring lanes, eight
+// elements (one 16-byte load) each, so the norm is a sum over LPH lanes and
+// the partner of a half-split rotation sits rot / 16 lanes away.
+//
+// The grid has two kinds of workgroups.  Query workgroups: a wavefront takes
+// one row and steps through its heads, HPW = 64 / LPH at a time, with the
+// row's cosines and sines in registers.  Cache workgroups: one (page, KV
+// head) each, found from the slots: the workgroup of row t goes on when t is
+// the first row of its page in the call, and gathers the rows of that page.
+// A page's scale is then one workgroup's business, whatever order the slots
+// come in: no atomics, no second launch.
+// ---------------------------------------------------------------------------
+constexpr int kAppendThreads = 256;
+constexpr int kAppendWaves = kAppendThreads / kLanes;
+
+// pos * f / (2 pi) less its nearest whole number, in turns.  The product of a
+// 31-bit position and a 24-bit frequency is rounded once; 1 / (2 pi) is taken
+// in two parts, so the angle's error stays near 1e-16 turns times the product.
+__device__ __forceinline__ double turns_of(double position, float freq) {
+  constexpr double kInv2Pi = 0.15915494309189535;        // 1 / (2 pi), nearest double
+  constexpr double kInv2PiLow = -9.8393383378404447e-18;  // and what is left of it
+  const double angle = position * (double)freq;
+  const double t = angle * kInv2Pi;
+  const double low = fma(angle, kInv2Pi, -t) + angle * kInv2PiLow;
+  return (t - rint(t)) + low;
+}
+
+// cos and sin of 2 pi t for |t| <= 1/2 (and a little over): quarter turns are
+// split off, the rest (at most an eighth of a turn) goes through the Taylor
+// series, whose first left-out terms are below 3e-14 there.
+__device__ __forceinline__ void cos_sin_turns(double t, double* c, double* s) {
+  const double q = rint(4.0 * t);
+  const double x = (t - 0.25 * q) * 6.283185307179586;
+  const double y = x * x;
+  double si = fma(y, 1.0 / 6227020800.0, -1.0 / 39916800.0);
+  si = fma(y, si, 1.0 / 362880.0);
+  si = fma(y, si, -1.0 / 5040.0);
+  si = fma(y, si, 1.0 / 120.0);
+  si = fma(y, si, -1.0 / 6.0);
+  si = fma(x * y, si, x);
+  double co = fma(y, -1.0 / 87178291200.0, 1.0 / 479001600.0);
+  co = fma(y, co, -1.0 / 3628800.0);
+  co = fma(y, co, 1.0 / 40320.0);
+  co = fma(y, co, -1.0 / 720.0);
+  co = fma(y, co, 1.0 / 24.0);
+  co = fma(y, co, -0.5);
+  co = fma(y, co, 1.0);
+  const int k = (int)q & 3;
+  const double cc = (k & 1) ? si : co, ss = (k & 1) ? co : si;
+  *c = (k == 1 || k == 2) ? -cc : cc;
+  *s = (k >= 2) ? -ss : ss;
+}
+
+// x / scale as an E4M3 code: nearest, ties to even, saturating, NaN to NaN.
+// One rounding, from 64 bits: the code is the whole number of steps of the
+// value's binade (2^(e-3), e >= -6) plus the binade's first code.
+__device__ __forceinline__ uint32_t e4m3_code(double x) {
+  const uint64_t bits = (uint64_t)__double_as_longlong(x);
+  const uint32_t sign = (uint32_t)(bits >> 63) << 7;
+  if (x != x) return sign | 0x7Fu;
+  const double a = fmin(fabs(x), 448.0);
+  int e = (int)(((uint64_t)__double_as_longlong(a) >> 52)) - 1023;
+  e = e < -6 ? -6 : e;
+  const double inv_step = __longlong_as_double((long long)(uint64_t)(1023 + 3 - e) << 52);
+  return sign | (uint32_t)((e + 7) * 8 + (int)rint(a * inv_step) - 8);
+}
+
+__device__ __forceinline__ double e4m3_value(uint32_t code) {
+  const uint32_t m = code & 7, e = (code >> 3) & 15;
+  if ((code & 0x7F) == 0x7F) return __longlong_as_double(0x7FF8000000000000ll);
+  const double v = e ? ldexp(8.0 + m, (int)e - 10) : ldexp((double)m, -9);
+  return code & 0x80 ? -v : v;
+}
+
+// The smallest power of two s with amax <= 448 s, at least 2^-60.
+__device__ __forceinline__ double page_scale_for(double amax) {
+  if (!(amax > 0.0)) return 0x1p-60;
+  const uint64_t bits = (uint64_t)__double_as_longlong(amax);
+  const int e = (int)(bits >> 52) - 1023;
+  const int up = (bits & 0xFFFFFFFFFFFFFull) > 0xC000000000000ull;  // mantissa above 1.75 = 448 / 256
+  const int es = e - 8 + up;
+  return es <= -60 ? 0x1p-60 : __longlong_as_double((long long)(uint64_t)(1023 + es) << 52);
+}
+
+__device__ __forceinline__ half8 load_half8(const uint16_t* p) {
+  return *reinterpret_cast<const half8*>(p);
+}
+
+// T: float for queries, double for keys.  The norm and rotation of eight
+// elements of a head; `lane_at` is the lane's place among the head's LPH.
+// cs: cosines and sines of the lane's own angles.
+template <typename T, int DIM>
+struct Rotor {
+  T c[8], s[8];  // half-split: one per element; interleaved: entries 0 .. 3
+  bool turned;   // the lane's elements are rotated
+
+  __device__ __forceinline__ void angles(const RopeAppendArgs& a, int lane_at, double position) {
+    const int d0 = lane_at * 8, half = a.rot / 2;
+    turned = d0 < a.rot;
+    if (!turned) return;
+    const int n = a.interleaved ? 4 : 8;
+    const int j0 = a.interleaved ? d0 / 2 : d0 < half ? d0 : d0 - half;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i < n) {
+        const double t = turns_of(position, a.inv_freq[j0 + i]);
+        if constexpr (sizeof(T) == 8) {
+          cos_sin_turns(t, &c[i], &s[i]);
+        } else {
+          // the hardware's functions take turns; their error (below 2^-20) is
+          // far under the FP16 step of the result
+          c[i] = __builtin_amdgcn_cosf((float)t);
+          s[i] = __builtin_amdgcn_sinf((float)t);
+        }
+      }
+    }
+  }
+
+  // x: the raw elements; returns the normed and rotated ones
+  __device__ __forceinline__ void turn(const RopeAppendArgs& a, int lane_at, const half8& x,
+                                       const uint16_t* weight, T out[8]) const {
+    constexpr int LPH = DIM / 8;
+    T r = T(1);
+    if (weight) {
+      T sum = T(0);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum += (T)x[i] * (T)x[i];
+#pragma unroll
+      for (int d = 1; d < LPH; d <<= 1) sum += __shfl_xor(sum, d);
+      if constexpr (sizeof(T) == 8)
+        r = 1.0 / sqrt(sum * (1.0 / DIM) + a.eps);
+      else
+        r = 1.0f / sqrtf(sum * (1.0f / DIM) + (float)a.eps);
+      const half8 w = load_half8(weight + lane_at * 8);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out[i] = (T)x[i] * r * (T)w[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) out[i] = (T)x[i];
+    }
+    if (a.rot == 0) return;
+    if (a.interleaved) {
+      if (turned) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const T u = out[2 * i], v = out[2 * i + 1];
+          out[2 * i] = u * c[i] - v * s[i];
+          out[2 * i + 1] = v * c[i] + u * s[i];
+        }
+      }
+    } else {
+      // the other half of each pair: rot / 16 lanes up (first half) or down
+      const int step = a.rot / 16, lane = threadIdx.x & 63;
+      const bool first = lane_at < step;
+      const int from = !turned ? lane : first ? lane + step : lane - step;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const T other = __shfl(out[i], from);
+        if (turned) out[i] = first ? out[i] * c[i] - other * s[i] : out[i] * c[i] + other * s[i];
+      }
+    }
+  }
+};
+
+template <int DIM>
+__device__ __forceinline__ void append_queries(const RopeAppendArgs& a, int wg, int waves_per_row,
+                                               int steps) {
+  constexpr int LPH = DIM / 8, HPW = kLanes / LPH;
+  const int lane = threadIdx.x & 63, lane_at = lane % LPH;
+  const int64_t wave = (int64_t)wg * kAppendWaves + (threadIdx.x >> 6);
+  const int64_t row = wave / waves_per_row;
+  if (row >= a.rows) return;  // a whole wavefront; no barrier follows
+  Rotor<float, DIM> rotor;
+  if (a.rot) rotor.angles(a, lane_at, (double)a.positions[row]);
+  const int h0 = (int)(wave % waves_per_row) * steps * HPW + lane / LPH;
+  for (int i = 0; i < steps; ++i) {
+    const int h = h0 + i * HPW;
+    const bool in = h < a.q_heads;
+    half8 x = {};
+    if (in) x = load_half8(a.qkv + row * a.qkv_stride + (int64_t)h * DIM + lane_at * 8);
+    float out[8];
+    rotor.turn(a, lane_at, x, a.q_weight, out);
+    half8 y;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = (_Float16)out[e];
+    if (in) *reinterpret_cast<half8*>(a.q_out + row * a.q_stride + (int64_t)h * DIM + lane_at * 8) = y;
+  }
+}
+
+// Sixteen old codes at one place, rounded again to a larger scale.
+__device__ __forceinline__ u32x4 recode16(u32x4 c, double ratio) {
+  u32x4 o;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) r |= e4m3_code(e4m3_value((c[w] >> (8 * b)) & 255) * ratio) << (8 * b);
+    o[w] = r;
+  }
+  return o;
+}
+
+template <int DIM>
+__device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, int head) {
+  constexpr int LPH = DIM / 8;
+  constexpr int RPS = kAppendThreads / LPH;  // rows a step of the workgroup takes
+  constexpr int STEPS = kKvPage / RPS;
+  __shared__ int32_t s_row[kKvPage];      // the row at each offset of the page, -1: none
+  __shared__ int32_t s_list[kKvPage];     // the offsets that are written, in order
+  __shared__ int32_t s_earlier, s_count;
+  __shared__ double s_max[2][kAppendWaves];
+  __shared__ __attribute__((aligned(16))) uint8_t s_v[DIM * kKvPage];
+  const int tid = threadIdx.x, lane = tid & 63, lane_at = tid % LPH;
+
+  const int32_t slot0 = a.slots[row0];
+  if (slot0 < 0 || slot0 >= a.cache.pages * kKvPage) return;
+  const int32_t page = slot0 / kKvPage;
+  auto same_page = [&](int t) {
+    const int32_t s = a.slots[t];
+    return s >= 0 && s / kKvPage == page;
+  };
+  if (row0 > 0 && same_page(row0 - 1)) return;  // not the first of a run of rows
+
+  if (tid < kKvPage) s_row[tid] = -1;
+  if (tid == 0) s_earlier = 0;
+  __syncthreads();
+  for (int t = tid; t < a.rows; t += kAppendThreads) {
+    if (same_page(t)) {
+      if (t < row0) s_earlier = 1;
+      atomicMax(&s_row[a.slots[t] % kKvPage], t);
+    }
+  }
+  __syncthreads();
+  if (s_earlier) return;  // an earlier row's workgroup has the page
+  if (tid < kKvPage) {
+    const uint64_t taken = __ballot(s_row[tid] >= 0);
+    if (s_row[tid] >= 0) s_list[__popcll(taken & ((1ull << tid) - 1))] = tid;
+    if (tid == 0) s_count = __popcll(taken);
+  }
+  __syncthreads();
+  const int count = s_count;
+  const bool fresh = s_row[0] >= 0;
+  const int64_t block = (int64_t)page * a.cache.heads + head;
+  uint8_t* const kb = a.cache.k + block * (kKvPage * DIM);
+  uint8_t* const vb = a.cache.v + block * (kKvPage * DIM);
+  const double old_k = fresh ? 0.0 : (double)a.cache.k_scale[block];
+  const double old_v = fresh ? 0.0 : (double)a.cache.v_scale[block];
+
+  // the keys of one step: eight elements of row s_list[i]
+  auto key_of = [&](int i, double out[8]) {
+    const int t = s_row[s_list[i < count ? i : 0]];
+    Rotor<double, DIM> rotor;
+    if (a.rot) rotor.angles(a, lane_at, (double)a.positions[t]);
+    rotor.turn(a, lane_at, load_half8(a.qkv + t * a.qkv_stride + (int64_t)(a.q_heads + head) * DIM + lane_at * 8),
+               a.k_weight, out);
+  };
+  auto value_of = [&](int i) {
+    const int t = s_row[s_list[i < count ? i : 0]];
+    return load_half8(a.qkv + t * a.qkv_stride + (int64_t)(a.q_heads + a.cache.heads + head) * DIM +
+                      lane_at * 8);
+  };
+
+  // amax over the finite new values; the first step's keys stay in registers
+  // (a verify block or less), later ones are computed again below
+  double first[8], kmax = 0.0, vmax = 0.0;
+  half8 first_v;
+#pragma unroll 1
+  for (int st = 0; st < STEPS && st * RPS < count; ++st) {
+    const int i = st * RPS + tid / LPH;
+    double key[8];
+    key_of(i, key);
+    const half8 val = value_of(i);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const double k = fabs(key[e]), v = fabs((double)val[e]);
+      if (k < __builtin_inf()) kmax = fmax(kmax, k);
+      if (v < __builtin_inf()) vmax = fmax(vmax, v);
+      if (st == 0) first[e] = key[e];
+    }
+    if (st == 0) first_v = val;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    kmax = fmax(kmax, __shfl_xor(kmax, d));
+    vmax = fmax(vmax, __shfl_xor(vmax, d));
+  }
+  if (lane == 0) s_max[0][tid >> 6] = kmax, s_max[1][tid >> 6] = vmax;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kAppendWaves; ++w) {
+    kmax = fmax(kmax, s_max[0][w]);
+    vmax = fmax(vmax, s_max[1][w]);
+  }
+  const double need_k = page_scale_for(kmax), need_v = page_scale_for(vmax);
+  const double new_k = old_k > need_k ? old_k : need_k, new_v = old_v > need_v ? old_v : need_v;
+  const bool grow_k = old_k > 0.0 && new_k > old_k, grow_v = old_v > 0.0 && new_v > old_v;
+  const double inv_k = 1.0 / new_k, inv_v = 1.0 / new_v;
+
+  // keys: 8 codes per lane, two lanes make a 16-byte unit of the layout
+  if (grow_k) {
+    const double ratio = old_k / new_k;
+    for (int u = tid; u < (DIM / 16) * kKvPage; u += kAppendThreads) {
+      if (s_row[u % kKvPage] >= 0) continue;
+      u32x4* p = reinterpret_cast<u32x4*>(kb + u * 16);
+      *p = recode16(*p, ratio);
+    }
+  }
+#pragma unroll 1
+  for (int st = 0; st < STEPS && st * RPS < count; ++st) {
+    const int i = st * RPS + tid / LPH;
+    double key[8];
+    half8 val;
+    if (st == 0) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) key[e] = first[e];
+      val = first_v;
+    } else {
+      key_of(i, key);
+      val = value_of(i);
+    }
+    if (i < count) {
+      const int off = s_list[i], place = ((off >> 2) & 3) * 16 + (off >> 4) * 4 + (off & 3);
+      uint32_t w[2] = {0, 0};
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        w[e >> 2] |= e4m3_code(key[e] * inv_k) << (8 * (e & 3));
+        s_v[(lane_at * 8 + e) * kKvPage + place] = (uint8_t)e4m3_code((double)val[e] * inv_v);
+      }
+      uint2 pair;
+      pair.x = w[0], pair.y = w[1];
+      *reinterpret_cast<uint2*>(kb + (lane_at >> 1) * (kKvPage * 16) + off * 16 + (lane_at & 1) * 8) = pair;
+    }
+  }
+  __syncthreads();
+
+  // values: 16-byte segments (dimension d, group g) of the tokens 16 t + 4 g + r
+  const double ratio_v = grow_v ? old_v / new_v : 1.0;
+  for (int u = tid; u < DIM * 4; u += kAppendThreads) {
+    const int g = u & 3;
+    uint32_t fresh_bytes = 0;  // bit 4 t + r: token 16 t + 4 g + r is new
+#pragma unroll
+    for (int j = 0; j < 16; ++j) fresh_bytes |= (uint32_t)(s_row[(j >> 2) * 16 + g * 4 + (j & 3)] >= 0) << j;
+    if (!fresh_bytes && !grow_v) continue;
+    uint8_t* const p = vb + u * 16;
+    u32x4 c = *reinterpret_cast<const u32x4*>(s_v + u * 16);
+    if (fresh_bytes != 0xFFFFu) {
+      u32x4 o = *reinterpret_cast<const u32x4*>(p);
+      if (grow_v) o = recode16(o, ratio_v);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const uint32_t bits = (fresh_bytes >> (4 * t)) & 15;
+        const uint32_t mask = (bits & 1 ? 0xFFu : 0) | (bits & 2 ? 0xFF00u : 0) |
+                              (bits & 4 ? 0xFF0000u : 0) | (bits & 8 ? 0xFF000000u : 0);
+        c[t] = (c[t] & mask) | (o[t] & ~mask);
+      }
+    }
+    *reinterpret_cast<u32x4*>(p) = c;
+  }
+  if (tid == 0) {
+    a.cache.k_scale[block] = (float)new_k;
+    a.cache.v_scale[block] = (float)new_v;
+  }
+}
+
+template <int DIM>
+__global__ __launch_bounds__(kAppendThreads) void rope_append_kernel(RopeAppendArgs a, int cache_wgs,
+                                                                     int waves_per_row, int steps) {
+  if ((int)blockIdx.x < cache_wgs)
+    append_page<DIM>(a, (int)blockIdx.x / a.cache.heads, (int)blockIdx.x % a.cache.heads);
+  else
+    append_queries<DIM>(a, (int)blockIdx.x - cache_wgs, waves_per_row, steps);
+}
+
+template <int DIM>
+hipError_t launch_append(const RopeAppendArgs& a) {
+  constexpr int HPW = kLanes / (DIM / 8);
+  // heads per wavefront: one step of HPW while that leaves fewer wavefronts
+  // than 8 a CU, else more, so that a row's angles serve more heads
+  const int groups = (a.q_heads + HPW - 1) / HPW;
+  int64_t steps = (int64_t)a.rows * groups / 2048;
+  steps = steps < 1 ? 1 : steps > groups ? groups : steps;
+  const int waves_per_row = (int)((groups + steps - 1) / steps);
+  const int64_t cache_wgs = (int64_t)a.rows * a.cache.heads;
+  const int64_t query_wgs = ((int64_t)a.rows * waves_per_row + kAppendWaves - 1) / kAppendWaves;
+  rope_append_kernel<DIM><<<dim3((uint32_t)(cache_wgs + query_wgs)), dim3(kAppendThreads), 0,
+                            (hipStream_t)a.stream>>>(a, (int)cache_wgs, waves_per_row, (int)steps);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_plan_round(const PlanRoundArgs& a) {
+  plan_round_kernel<<<dim3(1), dim3(kPlanThreads), 0, (hipStream_t)a.stream>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_rope_append(const RopeAppendArgs& a) {
+  return a.cache.dim == 64 ? launch_append<64>(a) : a.cache.dim == 128 ? launch_append<128>(a) : launch_append<256>(a);
+}
+
+}  // namespace qpn

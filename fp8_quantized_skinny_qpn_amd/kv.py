@@ -1,0 +1,277 @@
+"""Thin ctypes binding of the speculative-round operators (the C ABI in include/qpn_kv.h).
+
+The operators around the packed-weight products of ``qpn``: page tables of a round, the cache
+append with query/key norms and rotation, attention over an 8-bit paged KV cache, and the
+verification of sampled drafts.  As in ``qpn``, argument marshalling only: every step of the
+computation runs in the HIP kernels of libqpn.so, and there is no fallback of any kind.
+
+One round, on the device throughout::
+
+    r = kv.plan_round(before, rows, held, table, free_pages, free_count, capacity)
+    qkv = qpn.gemm(w_qkv, x)
+    q = kv.rope_append(cache, qkv, q_heads, r.positions, r.slots, inv_freq, q_weight, k_weight)
+    y = kv.attention(cache, q, r.row_start, r.seq_lens, table, max_rows)
+    ...                                    # O, gate/up, down, lm_head
+    accepted, token, prob = kv.verify_sampled(logits, tokens, r.row_start, accept_u, sample_u)
+"""
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from .qpn import LIB_PATH, QpnError, _empty, _torch_stream, check, lib  # noqa: F401
+
+PAGE = 64
+SCRATCH_ZEROED = 65536
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32)]
+
+
+def _bind():
+    c = ctypes
+    vp, i64, sz, i32, f64, f32 = c.c_void_p, c.c_int64, c.c_size_t, c.c_int, c.c_double, c.c_float
+    cp = c.POINTER(_Cache)
+    sig = {
+        "qpn_kv_plan_round": ([vp, vp, vp, i32, vp, i64, i32, vp, i64, vp, i32, vp, vp, vp, vp, vp, vp, vp], i32),
+        "qpn_kv_rope_append": ([cp, vp, i64, i32, i32, vp, vp, f64, vp, i32, i32, vp, vp, vp, i64, vp], i32),
+        "qpn_kv_attention_scratch_bytes": ([i32, i32, i32, i32, i32, i32], sz),
+        "qpn_kv_attention": ([cp, vp, i64, vp, i64, i32, i32, i32, i32, vp, vp, vp, i64, i32, f32, i32, vp, sz, vp],
+                             i32),
+        "qpn_kv_verify_scratch_bytes": ([i32, i32, i64], sz),
+        "qpn_kv_verify_sampled": ([vp, i64, vp, i64, vp, vp, i32, i32, i64, f64, vp, vp, vp, vp, vp, vp, sz, vp],
+                                  i32),
+    }
+    for name, (args, res) in sig.items():
+        f = getattr(lib, name)
+        f.argtypes = args
+        f.restype = res
+    return tuple(sig)
+
+
+# Symbols the C header declares.
+EXPORTED = _bind()
+
+
+def _need(t, dtype, dim, what):
+    """A contiguous device tensor of this type and rank."""
+    if not (t.is_cuda and t.dtype == dtype and t.dim() == dim and t.is_contiguous()):
+        raise ValueError(f"{what} must be a contiguous {dim}-D {dtype} CUDA tensor")
+    return t.data_ptr()
+
+
+def _rows(t, what):
+    """(pointer, row stride) of FP16 rows: unit stride within a row."""
+    if not (t.is_cuda and t.dtype == torch.float16 and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1)):
+        raise ValueError(f"{what} must be a 2-D float16 CUDA tensor with unit stride in its rows")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+
+
+def _table(t, requests):
+    if not (t.is_cuda and t.dtype == torch.int32 and t.dim() == 2
+            and (t.stride(1) == 1 or t.shape[1] <= 1 or t.numel() == 0)):
+        raise ValueError("the page table must be a 2-D int32 CUDA tensor with unit stride in its rows")
+    if t.shape[0] != requests:
+        raise ValueError(f"the page table has {t.shape[0]} rows for {requests} requests")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 and t.shape[1] else max(t.shape[1], 1), t.shape[1]
+
+
+# Scratch of attention and verification, one per (device, stream): its zeroed
+# head is left zero by every call, the rest holds anything.  Allocated and
+# zeroed on the stream that uses it; a replaced buffer lives until the work
+# queued on that stream is done.
+_scratches = {}
+
+
+def scratch(nbytes: int, device, stream) -> torch.Tensor:
+    """The cached scratch of at least nbytes for `stream` (a torch stream) on `device`."""
+    key = (device.index, stream.cuda_stream)
+    s = _scratches.get(key)
+    if s is None or s.numel() < nbytes:
+        with torch.cuda.stream(stream):
+            new = torch.empty(max(nbytes, SCRATCH_ZEROED), dtype=torch.uint8, device=device)
+            new[:SCRATCH_ZEROED].zero_()
+        if s is not None:
+            s.record_stream(stream)
+        _scratches[key] = s = new
+    return s
+
+
+class KvCache:
+    """One layer's cache: pages of 64 tokens, E4M3 codes with a scale per page and head.
+
+    k: float8_e4m3fn [pages, heads, dim / 16, 64, 16]: dimension 16 c + e of token t at [c, t, e];
+    v: float8_e4m3fn [pages, heads, dim, 64]: dimension d of token 16 t + 4 g + r at
+    [d, 16 g + 4 t + r]; k_scale, v_scale: float32 [pages, heads]."""
+
+    def __init__(self, k, v, k_scale, v_scale):
+        if k.dim() != 5 or k.shape[3] != PAGE or k.shape[4] != 16:
+            raise ValueError("keys must be [pages, heads, dim / 16, 64, 16]")
+        pages, heads, dim = k.shape[0], k.shape[1], k.shape[2] * 16
+        if tuple(v.shape) != (pages, heads, dim, PAGE):
+            raise ValueError("values must be [pages, heads, dim, 64]")
+        if tuple(k_scale.shape) != (pages, heads) or tuple(v_scale.shape) != (pages, heads):
+            raise ValueError("scales must be [pages, heads]")
+        f8 = torch.float8_e4m3fn
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self.pages, self.heads, self.dim = pages, heads, dim
+        self._c = _Cache(_need(k, f8, 5, "keys"), _need(v, f8, 4, "values"),
+                         _need(k_scale, torch.float32, 2, "key scales"),
+                         _need(v_scale, torch.float32, 2, "value scales"), pages, heads, dim)
+        self._ref = ctypes.byref(self._c)
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, device="cuda") -> "KvCache":
+        """A cache of pages no request holds yet."""
+        f8 = torch.float8_e4m3fn
+        return cls(torch.zeros((pages, heads, dim // 16, PAGE, 16), dtype=f8, device=device),
+                   torch.zeros((pages, heads, dim, PAGE), dtype=f8, device=device),
+                   torch.ones((pages, heads), device=device), torch.ones((pages, heads), device=device))
+
+
+@dataclass
+class Round:
+    """What plan_round writes: int32 device tensors."""
+    seq_lens: torch.Tensor    # [requests]
+    row_start: torch.Tensor   # [requests + 1]
+    held: torch.Tensor        # [requests]
+    free_count: torch.Tensor  # [1]
+    slots: torch.Tensor       # [capacity]
+    positions: torch.Tensor   # [capacity]
+
+    @classmethod
+    def empty(cls, requests: int, capacity: int, device="cuda") -> "Round":
+        e = lambda n: torch.empty(n, dtype=torch.int32, device=device)  # noqa: E731
+        return cls(e(requests), e(requests + 1), e(requests), e(1), e(capacity), e(capacity))
+
+
+def plan_round(before, rows, held, table, free_pages, free_count, capacity: int = None, out: Round = None,
+               stream=None) -> Round:
+    """Page tables, row_start, slots and positions of a round through qpn_kv_plan_round; the
+    table's new entries are written in place.  `capacity` (rows) or `out` is needed."""
+    i32 = torch.int32
+    n = before.shape[0]
+    ts = _torch_stream(stream)
+    if out is None:
+        if capacity is None:
+            raise ValueError("capacity or out is needed")
+        with torch.cuda.stream(ts):
+            out = Round.empty(n, capacity, before.device)
+    elif capacity is not None and capacity != out.slots.shape[0]:
+        raise ValueError(f"out has room for {out.slots.shape[0]} rows, not {capacity}")
+    if rows.shape[0] != n or held.shape[0] != n or out.seq_lens.shape[0] != n or out.held.shape[0] != n \
+            or out.row_start.shape[0] != n + 1 or out.positions.shape[0] != out.slots.shape[0] \
+            or free_count.numel() != 1 or out.free_count.numel() != 1:
+        raise ValueError("sizes of the requests' tensors do not agree")
+    tp, tstride, width = _table(table, n)
+    check(lib.qpn_kv_plan_round(
+        _need(before, i32, 1, "before"), _need(rows, i32, 1, "rows"), _need(held, i32, 1, "held"), n, tp, tstride,
+        width, _need(free_pages, i32, 1, "free_pages"), free_pages.shape[0], _need(free_count, i32, 1, "free_count"),
+        out.slots.shape[0], _need(out.seq_lens, i32, 1, "seq_lens"), _need(out.row_start, i32, 1, "row_start"),
+        _need(out.held, i32, 1, "held"), _need(out.free_count, i32, 1, "free_count"),
+        _need(out.slots, i32, 1, "slots"), _need(out.positions, i32, 1, "positions"), ts.cuda_stream))
+    return out
+
+
+def rope_append(cache: KvCache, qkv, q_heads: int, positions, slots, inv_freq, q_weight=None, k_weight=None,
+                eps: float = 1e-6, interleaved: bool = False, out=None, stream=None) -> torch.Tensor:
+    """Norms, rotation and cache append of QKV rows through qpn_kv_rope_append; returns the queries
+    [rows, q_heads * dim].  inv_freq: float32 [rot / 2] (None: no rotation)."""
+    d = cache.dim
+    rows = qkv.shape[0]
+    qp, qs = _rows(qkv, "qkv")
+    if qkv.shape[1] != (q_heads + 2 * cache.heads) * d:
+        raise ValueError(f"qkv has {qkv.shape[1]} columns for {q_heads} + 2 * {cache.heads} heads of {d}")
+    if positions.shape[0] != rows or slots.shape[0] != rows:
+        raise ValueError("positions and slots must have one entry per row")
+    for w in (q_weight, k_weight):
+        if w is not None and w.shape[0] != d:
+            raise ValueError(f"norm weights must have {d} elements")
+    ts = _torch_stream(stream)
+    if out is None:
+        out = _empty(ts, (rows, q_heads * d), torch.float16, qkv.device)
+    op, os = _rows(out, "out")
+    if tuple(out.shape) != (rows, q_heads * d):
+        raise ValueError(f"out must be [{rows}, {q_heads * d}]")
+    f16, i32 = torch.float16, torch.int32
+    check(lib.qpn_kv_rope_append(
+        cache._ref, qp, qs, rows, q_heads, None if q_weight is None else _need(q_weight, f16, 1, "q_weight"),
+        None if k_weight is None else _need(k_weight, f16, 1, "k_weight"), eps,
+        None if inv_freq is None else _need(inv_freq, torch.float32, 1, "inv_freq"),
+        0 if inv_freq is None else 2 * inv_freq.shape[0], interleaved, _need(positions, i32, 1, "positions"),
+        _need(slots, i32, 1, "slots"), op, os, ts.cuda_stream))
+    return out
+
+
+def attention_scratch_bytes(requests: int, max_rows: int, q_heads: int, heads: int, dim: int, width: int) -> int:
+    return int(lib.qpn_kv_attention_scratch_bytes(requests, max_rows, q_heads, heads, dim, width))
+
+
+def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scale: float = None, window: int = 0,
+              out=None, stream=None, scratch_=None) -> torch.Tensor:
+    """Attention of the rows q [rows, q_heads * dim] over the cache through qpn_kv_attention.
+    `max_rows`: the most rows of one request (a hint).  `scale` defaults to dim ** -0.5."""
+    d = cache.dim
+    n = seq_lens.shape[0]
+    if q.dim() != 2 or q.shape[1] % d:
+        raise ValueError(f"queries must be [rows, heads * {d}]")
+    if row_start.shape[0] != n + 1:
+        raise ValueError("row_start must have one entry more than seq_lens")
+    heads = q.shape[1] // d
+    qp, qs = _rows(q, "queries")
+    tp, tstride, width = _table(table, n)
+    ts = _torch_stream(stream)
+    if out is None:
+        out = _empty(ts, tuple(q.shape), torch.float16, q.device)
+    elif out.shape != q.shape:
+        raise ValueError("out must have the queries' shape")
+    yp, ys = _rows(out, "out")
+    if scratch_ is None:
+        need = lib.qpn_kv_attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
+        scratch_ = scratch(need if need < 1 << 63 else 0, q.device, ts)
+    check(lib.qpn_kv_attention(
+        cache._ref, qp, qs, yp, ys, heads, q.shape[0], n, max_rows, _need(row_start, torch.int32, 1, "row_start"),
+        _need(seq_lens, torch.int32, 1, "seq_lens"), tp, tstride, width, d ** -0.5 if scale is None else scale,
+        window, scratch_.data_ptr(), scratch_.numel(), ts.cuda_stream))
+    return out
+
+
+def verify_scratch_bytes(rows: int, requests: int, n: int) -> int:
+    return int(lib.qpn_kv_verify_scratch_bytes(rows, requests, n))
+
+
+def verify_sampled(logits, tokens, row_start, accept_u, sample_u, draft_logits=None, temperature: float = 1.0,
+                   out=None, stream=None, scratch_=None):
+    """(accepted int32 [requests], next int32 [requests], accept_prob float32 [rows]) through
+    qpn_kv_verify_sampled.  draft_logits None: a greedy drafter."""
+    rows, n = logits.shape
+    requests = row_start.shape[0] - 1
+    lp, ls = _rows(logits, "logits")
+    dp = ds = 0
+    if draft_logits is not None:
+        dp, ds = _rows(draft_logits, "draft_logits")
+        if draft_logits.shape != logits.shape:
+            raise ValueError("draft_logits must have the logits' shape")
+    if tokens.shape[0] != rows or accept_u.shape[0] != rows or sample_u.shape[0] != requests:
+        raise ValueError("tokens and accept_u need one entry per row, sample_u one per request")
+    if not temperature > 0:
+        raise ValueError("temperature must be positive")
+    ts = _torch_stream(stream)
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    if out is None:
+        out = (_empty(ts, (requests,), i32, dev), _empty(ts, (requests,), i32, dev), _empty(ts, (rows,), f32, dev))
+    accepted, token, prob = out
+    if accepted.shape[0] != requests or token.shape[0] != requests or prob.shape[0] != rows:
+        raise ValueError("out must be (accepted [requests], next [requests], accept_prob [rows])")
+    if scratch_ is None:
+        need = lib.qpn_kv_verify_scratch_bytes(rows, requests, n)
+        scratch_ = scratch(need if need < 1 << 63 else 0, dev, ts)
+    check(lib.qpn_kv_verify_sampled(
+        lp, ls, dp or None, ds, _need(tokens, i32, 1, "tokens"), _need(row_start, i32, 1, "row_start"), rows,
+        requests, n, 1.0 / temperature, _need(accept_u, f32, 1, "accept_u"), _need(sample_u, f32, 1, "sample_u"),
+        _need(accepted, i32, 1, "accepted"), _need(token, i32, 1, "next"), _need(prob, f32, 1, "accept_prob"),
+        scratch_.data_ptr(), scratch_.numel(), ts.cuda_stream))
+    return out
