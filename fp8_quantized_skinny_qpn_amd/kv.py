@@ -16,6 +16,7 @@ One round, on the device throughout::
 """
 import ctypes
 from dataclasses import dataclass
+from functools import lru_cache
 
 import torch
 
@@ -58,44 +59,65 @@ EXPORTED = _bind()
 
 def _need(t, dtype, dim, what):
     """A contiguous device tensor of this type and rank."""
-    if not (t.is_cuda and t.dtype == dtype and t.dim() == dim and t.is_contiguous()):
-        raise ValueError(f"{what} must be a contiguous {dim}-D {dtype} CUDA tensor")
-    return t.data_ptr()
+    if t.dtype is dtype and t.is_cuda and t.dim() == dim and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{what} must be a contiguous {dim}-D {dtype} CUDA tensor")
 
 
 def _rows(t, what):
     """(pointer, row stride) of FP16 rows: unit stride within a row."""
-    if not (t.is_cuda and t.dtype == torch.float16 and t.dim() == 2 and (t.stride(1) == 1 or t.shape[1] == 1)):
-        raise ValueError(f"{what} must be a 2-D float16 CUDA tensor with unit stride in its rows")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    if t.dtype is torch.float16 and t.is_cuda and t.dim() == 2:
+        (n, width), (stride, step) = t.shape, t.stride()
+        if step == 1 or width == 1:
+            return t.data_ptr(), stride if n > 1 else max(width, 1)
+    raise ValueError(f"{what} must be a 2-D float16 CUDA tensor with unit stride in its rows")
 
 
 def _table(t, requests):
-    if not (t.is_cuda and t.dtype == torch.int32 and t.dim() == 2
-            and (t.stride(1) == 1 or t.shape[1] <= 1 or t.numel() == 0)):
+    if not (t.dtype is torch.int32 and t.is_cuda and t.dim() == 2):
         raise ValueError("the page table must be a 2-D int32 CUDA tensor with unit stride in its rows")
-    if t.shape[0] != requests:
-        raise ValueError(f"the page table has {t.shape[0]} rows for {requests} requests")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 and t.shape[1] else max(t.shape[1], 1), t.shape[1]
+    (n, width), (stride, step) = t.shape, t.stride()
+    if not (step == 1 or width <= 1 or n == 0):
+        raise ValueError("the page table must be a 2-D int32 CUDA tensor with unit stride in its rows")
+    if n != requests:
+        raise ValueError(f"the page table has {n} rows for {requests} requests")
+    return t.data_ptr(), stride if n > 1 and width else max(width, 1), width
+
+
+def _raw_stream(stream) -> int:
+    """The HIP stream of a call: the given torch stream's, else the current device's current one.
+    (torch.cuda.current_stream() builds an object, which costs more than the rest of a call.)"""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 # Scratch of attention and verification, one per (device, stream): its zeroed
 # head is left zero by every call, the rest holds anything.  Allocated and
-# zeroed on the stream that uses it; a replaced buffer lives until the work
-# queued on that stream is done.
+# zeroed on the stream that uses it.  A buffer that grows is kept next to its
+# successor (at least twice its size), since a captured graph may hold it.
 _scratches = {}
+_outgrown = []
 
 
 def scratch(nbytes: int, device, stream) -> torch.Tensor:
     """The cached scratch of at least nbytes for `stream` (a torch stream) on `device`."""
-    key = (device.index, stream.cuda_stream)
+    return _scratch(nbytes, device, stream.cuda_stream, stream)
+
+
+def _scratch(nbytes: int, device, raw: int, stream) -> torch.Tensor:
+    key = (device.index, raw)
     s = _scratches.get(key)
     if s is None or s.numel() < nbytes:
+        stream = _torch_stream(stream)
+        nbytes = max(nbytes, SCRATCH_ZEROED, 0 if s is None else 2 * s.numel())
         with torch.cuda.stream(stream):
-            new = torch.empty(max(nbytes, SCRATCH_ZEROED), dtype=torch.uint8, device=device)
+            new = torch.empty(nbytes, dtype=torch.uint8, device=device)
             new[:SCRATCH_ZEROED].zero_()
+            if torch.cuda.is_current_stream_capturing():
+                return new  # the graph's own: it is zeroed when the graph runs, not now
         if s is not None:
-            s.record_stream(stream)
+            _outgrown.append(s)
         _scratches[key] = s = new
     return s
 
@@ -147,6 +169,22 @@ class Round:
         e = lambda n: torch.empty(n, dtype=torch.int32, device=device)  # noqa: E731
         return cls(e(requests), e(requests + 1), e(requests), e(1), e(capacity), e(capacity))
 
+    def __setattr__(self, name, value):
+        self.__dict__["_args"] = None
+        self.__dict__[name] = value
+
+    def _checked(self):
+        """(requests, capacity, the six pointers), checked once after a field is set."""
+        if self._args is None:
+            n, cap = self.seq_lens.shape[0], self.slots.shape[0]
+            if self.held.shape[0] != n or self.row_start.shape[0] != n + 1 \
+                    or self.positions.shape[0] != cap or self.free_count.numel() != 1:
+                raise ValueError("sizes of the requests' tensors do not agree")
+            self.__dict__["_args"] = (n, cap) + tuple(
+                _need(getattr(self, k), torch.int32, 1, k)
+                for k in ("seq_lens", "row_start", "held", "free_count", "slots", "positions"))
+        return self._args
+
 
 def plan_round(before, rows, held, table, free_pages, free_count, capacity: int = None, out: Round = None,
                stream=None) -> Round:
@@ -154,25 +192,21 @@ def plan_round(before, rows, held, table, free_pages, free_count, capacity: int 
     table's new entries are written in place.  `capacity` (rows) or `out` is needed."""
     i32 = torch.int32
     n = before.shape[0]
-    ts = _torch_stream(stream)
     if out is None:
         if capacity is None:
             raise ValueError("capacity or out is needed")
-        with torch.cuda.stream(ts):
+        with torch.cuda.stream(_torch_stream(stream)):
             out = Round.empty(n, capacity, before.device)
-    elif capacity is not None and capacity != out.slots.shape[0]:
-        raise ValueError(f"out has room for {out.slots.shape[0]} rows, not {capacity}")
-    if rows.shape[0] != n or held.shape[0] != n or out.seq_lens.shape[0] != n or out.held.shape[0] != n \
-            or out.row_start.shape[0] != n + 1 or out.positions.shape[0] != out.slots.shape[0] \
-            or free_count.numel() != 1 or out.free_count.numel() != 1:
+    requests, cap, seq_p, start_p, held_p, count_p, slots_p, pos_p = out._checked()
+    if capacity is not None and capacity != cap:
+        raise ValueError(f"out has room for {cap} rows, not {capacity}")
+    if requests != n or rows.shape[0] != n or held.shape[0] != n or free_count.numel() != 1:
         raise ValueError("sizes of the requests' tensors do not agree")
     tp, tstride, width = _table(table, n)
     check(lib.qpn_kv_plan_round(
         _need(before, i32, 1, "before"), _need(rows, i32, 1, "rows"), _need(held, i32, 1, "held"), n, tp, tstride,
         width, _need(free_pages, i32, 1, "free_pages"), free_pages.shape[0], _need(free_count, i32, 1, "free_count"),
-        out.slots.shape[0], _need(out.seq_lens, i32, 1, "seq_lens"), _need(out.row_start, i32, 1, "row_start"),
-        _need(out.held, i32, 1, "held"), _need(out.free_count, i32, 1, "free_count"),
-        _need(out.slots, i32, 1, "slots"), _need(out.positions, i32, 1, "positions"), ts.cuda_stream))
+        cap, seq_p, start_p, held_p, count_p, slots_p, pos_p, _raw_stream(stream)))
     return out
 
 
@@ -190,9 +224,8 @@ def rope_append(cache: KvCache, qkv, q_heads: int, positions, slots, inv_freq, q
     for w in (q_weight, k_weight):
         if w is not None and w.shape[0] != d:
             raise ValueError(f"norm weights must have {d} elements")
-    ts = _torch_stream(stream)
     if out is None:
-        out = _empty(ts, (rows, q_heads * d), torch.float16, qkv.device)
+        out = _empty(_torch_stream(stream), (rows, q_heads * d), torch.float16, qkv.device)
     op, os = _rows(out, "out")
     if tuple(out.shape) != (rows, q_heads * d):
         raise ValueError(f"out must be [{rows}, {q_heads * d}]")
@@ -202,10 +235,11 @@ def rope_append(cache: KvCache, qkv, q_heads: int, positions, slots, inv_freq, q
         None if k_weight is None else _need(k_weight, f16, 1, "k_weight"), eps,
         None if inv_freq is None else _need(inv_freq, torch.float32, 1, "inv_freq"),
         0 if inv_freq is None else 2 * inv_freq.shape[0], interleaved, _need(positions, i32, 1, "positions"),
-        _need(slots, i32, 1, "slots"), op, os, ts.cuda_stream))
+        _need(slots, i32, 1, "slots"), op, os, _raw_stream(stream)))
     return out
 
 
+@lru_cache(maxsize=1024)
 def attention_scratch_bytes(requests: int, max_rows: int, q_heads: int, heads: int, dim: int, width: int) -> int:
     return int(lib.qpn_kv_attention_scratch_bytes(requests, max_rows, q_heads, heads, dim, width))
 
@@ -223,22 +257,23 @@ def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scal
     heads = q.shape[1] // d
     qp, qs = _rows(q, "queries")
     tp, tstride, width = _table(table, n)
-    ts = _torch_stream(stream)
+    raw = _raw_stream(stream)
     if out is None:
-        out = _empty(ts, tuple(q.shape), torch.float16, q.device)
+        out = _empty(_torch_stream(stream), tuple(q.shape), torch.float16, q.device)
     elif out.shape != q.shape:
         raise ValueError("out must have the queries' shape")
     yp, ys = _rows(out, "out")
     if scratch_ is None:
-        need = lib.qpn_kv_attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
-        scratch_ = scratch(need if need < 1 << 63 else 0, q.device, ts)
+        need = attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
+        scratch_ = _scratch(need if need < 1 << 63 else 0, q.device, raw, stream)
     check(lib.qpn_kv_attention(
         cache._ref, qp, qs, yp, ys, heads, q.shape[0], n, max_rows, _need(row_start, torch.int32, 1, "row_start"),
         _need(seq_lens, torch.int32, 1, "seq_lens"), tp, tstride, width, d ** -0.5 if scale is None else scale,
-        window, scratch_.data_ptr(), scratch_.numel(), ts.cuda_stream))
+        window, scratch_.data_ptr(), scratch_.numel(), raw))
     return out
 
 
+@lru_cache(maxsize=1024)
 def verify_scratch_bytes(rows: int, requests: int, n: int) -> int:
     return int(lib.qpn_kv_verify_scratch_bytes(rows, requests, n))
 
@@ -259,19 +294,20 @@ def verify_sampled(logits, tokens, row_start, accept_u, sample_u, draft_logits=N
         raise ValueError("tokens and accept_u need one entry per row, sample_u one per request")
     if not temperature > 0:
         raise ValueError("temperature must be positive")
-    ts = _torch_stream(stream)
+    raw = _raw_stream(stream)
     dev, i32, f32 = logits.device, torch.int32, torch.float32
     if out is None:
+        ts = _torch_stream(stream)
         out = (_empty(ts, (requests,), i32, dev), _empty(ts, (requests,), i32, dev), _empty(ts, (rows,), f32, dev))
     accepted, token, prob = out
     if accepted.shape[0] != requests or token.shape[0] != requests or prob.shape[0] != rows:
         raise ValueError("out must be (accepted [requests], next [requests], accept_prob [rows])")
     if scratch_ is None:
-        need = lib.qpn_kv_verify_scratch_bytes(rows, requests, n)
-        scratch_ = scratch(need if need < 1 << 63 else 0, dev, ts)
+        need = verify_scratch_bytes(rows, requests, n)
+        scratch_ = _scratch(need if need < 1 << 63 else 0, dev, raw, stream)
     check(lib.qpn_kv_verify_sampled(
         lp, ls, dp or None, ds, _need(tokens, i32, 1, "tokens"), _need(row_start, i32, 1, "row_start"), rows,
         requests, n, 1.0 / temperature, _need(accept_u, f32, 1, "accept_u"), _need(sample_u, f32, 1, "sample_u"),
         _need(accepted, i32, 1, "accepted"), _need(token, i32, 1, "next"), _need(prob, f32, 1, "accept_prob"),
-        scratch_.data_ptr(), scratch_.numel(), ts.cuda_stream))
+        scratch_.data_ptr(), scratch_.numel(), raw))
     return out
