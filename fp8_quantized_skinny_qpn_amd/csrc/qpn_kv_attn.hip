@@ -42,30 +42,30 @@ constexpr int kRsrc = 0x00020000;
 
 constexpr float kMaxSlack = 8.0f;     // how far (log2) a score may pass the running maximum
 constexpr float kScaleSlack = 64.0f;  // and a page's V scale the running one
+constexpr float kScaleLeast = 0x1p-20f;
 constexpr float kLowest = -3e38f;     // the running maximum before any score
 
-// wavefronts of a workgroup, few rows: two a SIMD while their registers allow
-// it (a spilled register is a load that waits behind the page's)
-constexpr int few_waves(int dim, int tiles) { return dim * tiles <= 384 ? 8 : 4; }
-constexpr int kManyWaves = 4;  // and many
+// wavefronts of a workgroup, few rows: one per 16 dimensions up to eight
+constexpr int few_waves(int dim) { return dim == 64 ? 4 : 8; }
+constexpr int kManyWaves = 4;  // and many rows
 constexpr int kMinPiecePages = 8;
 constexpr int kMaxPieces = 1024;   // pieces of a call with cut segments
-constexpr int kJoinDirect = 8;     // pieces joined in one step
+constexpr int kJoinDirect = 16;    // pieces joined in one step
 constexpr int kCounterStep = 8;    // 32-bit words between counters
 static_assert((size_t)kMaxPieces * 2 * kCounterStep * 4 <= kKvZeroedBytes, "two counters per piece");
 
-// The form and the 16-row tiles of a wavefront for `rows` rows of a KV head
-// (query rows x group).
+// The form and the 16-row tiles of a wavefront (of a workgroup, few rows) for
+// `rows` rows of a KV head (query rows x group).
+constexpr int kFewTiles = 3;
 struct Form {
   bool many;
   int tiles;
   int rows() const { return 16 * tiles * (many ? kManyWaves : 1); }
 };
 inline Form form_for(int64_t rows, int dim) {
-  const int few = dim == 256 ? 1 : 3;
   const int64_t t = (rows + 15) / 16;
-  if (t <= few) return {false, t < 1 ? 1 : (int)t};
-  return {true, t <= kManyWaves ? 1 : 2};
+  if (t <= kFewTiles) return {false, t < 1 ? 1 : (int)t};
+  return {true, t <= kManyWaves ? 1 : t <= 2 * kManyWaves || dim == 256 ? 2 : 3};
 }
 
 struct AttnLaunch {
@@ -243,8 +243,9 @@ __device__ __forceinline__ half8 to_half8(const float4v& a, const float4v& b) {
 // each tile, and the extremes over its rows.
 template <int RT>
 struct View {
-  int lim[RT], low[RT];
+  int lim[RT], window;
   int lim_min, lim_max, low_min, low_max;
+  __device__ __forceinline__ int low(int rt) const { return window > 0 ? max(0, lim[rt] - window) : 0; }
 };
 
 // Bits of the tokens [low, lim) among the 32 from `base` on, from the lane's
@@ -278,76 +279,42 @@ struct Rows {
     }
   }
 
-  // Whether a page is an ordinary one: every row sees all of it, and its
-  // scales are positive and in proportion.  (Uniform over the wavefront.)
+  // Whether every row sees all of the page, whose scales are positive and in
+  // proportion.  (Uniform over the wavefront.)
   __device__ __forceinline__ bool ordinary(float kc, float vs, int base, const View<RT>& see) const {
     return base + kKvPage <= see.lim_min && base >= see.low_max && kc > 0.0f && vs <= vref * kScaleSlack &&
-           vs >= vref * 0x1p-20f;
+           vs >= vref * kScaleLeast;
   }
 
-  // One ordinary page (EDGE: any page), in two halves of 32 tokens, so that a
-  // half's scores, not a page's, are held in registers beside the sums.
-  //   key(u, t): the codes of unit 4 u + g of token 16 t + c16;
-  //   query(k, rt): the B operand of k-step k (load_query);
-  //   value(d): the codes of dimension 16 d + c16, tokens 16 t + 4 g + r;
-  //   kc: the factor of the scores in units of log2 e, vs: the V scale;
-  //   fetch(): called when the last key has been used.
-  template <bool EDGE, typename Key, typename Query, typename Value, typename Fetch>
-  __device__ __forceinline__ void page(const Key& key, const Query& query, const Value& value, const Fetch& fetch,
-                                       float kc, float vs, int base, int g, const View<RT>& see) {
-    bool plain = true;
-    float sign = 1.0f;
-    if constexpr (EDGE) {
-      // a negative factor moves to the scores; for 0 any does, with zeros
-      if (!(kc > 0.0f)) {
-        sign = kc == 0.0f ? 0.0f : -1.0f;
-        kc = kc == 0.0f ? 1.0f : -kc;
-      }
-      if (vs > vref * kScaleSlack) {
-        const float f = vref / vs;
-        vref = vs;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[d][rt] *= f;
-      }
-      plain = vs >= vref * 0x1p-20f;
+  // What a page that is not an ordinary one needs beside masks.
+  struct Edge {
+    float sign;     // of the scores
+    bool nothing;   // the values count for nothing
+  };
+  // Takes the scales of such a page to ordinary ones.
+  __device__ __forceinline__ Edge settle(float& kc, float& vs) {
+    Edge e{1.0f, false};
+    if (!(kc > 0.0f)) {  // a negative factor moves to the scores; for 0 any does, with zeros
+      e.sign = kc == 0.0f ? 0.0f : -1.0f;
+      kc = kc == 0.0f ? 1.0f : -kc;
     }
-    // weights times vs / vref = exp2(score - m + log2(vs / vref)), and their
-    // FP32 sum times vref / vs; where vs is out of proportion (or not
-    // positive) the values are multiplied instead
-    const float vrel = vs / vref;
-    const float lift = plain ? __builtin_amdgcn_logf(vrel) : 0.0f, drop = plain ? vref / vs : 1.0f;
+    if (vs > vref * kScaleSlack || (vs < vref * kScaleLeast && vs > vref * 0x1p-90f)) {
+      const float f = vref / vs;
+      vref = vs;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      float4v s[2][RT];
-      scores(key, query, half, s);
-      if (half == 1) fetch();
-      half8 p[RT];
-      if constexpr (EDGE) {
+      for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const uint32_t seen = seen_of(see.lim[rt], see.low[rt], base + 32 * half, g);
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-              const uint32_t ones = all_ones_if(seen, t, r);
-              const float x = s[t][rt][r] * sign;
-              s[t][rt][r] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & ones) | (0xFF800000u & ~ones));  // -inf
-            }
-        }
-      }
-      weigh(s, kc, lift, drop, p);
-      if constexpr (EDGE)
-        accumulate_edge(value, p, half, plain ? 1.0f : vrel, base + 32 * half, g, see);
-      else
-        accumulate(value, p, half);
+        for (int d = 0; d < DT; ++d) o[d][rt] *= f;
+    } else if (vs <= vref * kScaleLeast) {  // zero beside the others (a NaN goes on)
+      e.nothing = true;
+      vs = vref;
     }
+    return e;
   }
 
- private:
-  // S^T of half a page
+  // S^T of half a page.
+  //   key(u, t, h): operand h of the two of unit 4 u + g of token 16 t + c16;
+  //   query(k, rt): the B operand of k-step k (load_query).
   template <typename Key, typename Query>
   __device__ __forceinline__ void scores(const Key& key, const Query& query, int half, float4v (&s)[2][RT]) const {
 #pragma unroll
@@ -356,26 +323,40 @@ struct Rows {
       for (int rt = 0; rt < RT; ++rt) s[t][rt] = float4v{0, 0, 0, 0};
 #pragma unroll
     for (int u = 0; u < DIM / 64; ++u) {
-      half8 q[2][RT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        half8 q[RT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) q[h][rt] = query(2 * u + h, rt);
+        for (int rt = 0; rt < RT; ++rt) q[rt] = query(2 * u + h, rt);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        half8 kf[2];
-        decode_fp8_fragment(key(u, 2 * half + t), kf);
+        for (int t = 0; t < 2; ++t) {
+          const half8 kf = key(u, 2 * half + t, h);
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-            s[t][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[h], q[h][rt], s[t][rt], 0, 0, 0);
+          for (int rt = 0; rt < RT; ++rt) s[t][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[rt], s[t][rt], 0, 0, 0);
+        }
       }
     }
   }
 
+  // -inf for what a row does not see, from token `base` on.
+  __device__ __forceinline__ void mask(float4v (&s)[2][RT], float sign, int base, int g, const View<RT>& see) const {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const uint32_t seen = seen_of(see.lim[rt], see.low(rt), base, g);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t ones = all_ones_if(seen, t, r);
+          const float x = s[t][rt][r] * sign;
+          s[t][rt][r] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & ones) | (0xFF800000u & ~ones));
+        }
+    }
+  }
+
   // The weights of half a page's scores, as the B operands of the second
-  // product; the sums and maxima follow.
+  // product, times vs / vref: exp2(kc score - m + lift), lift = log2(vs / vref);
+  // their FP32 sum times vref / vs (drop) goes to the sums.
   __device__ __forceinline__ void weigh(float4v (&s)[2][RT], float kc, float lift, float drop, half8 (&p)[RT]) {
     float top[RT];
     bool raise = false;
@@ -417,94 +398,112 @@ struct Rows {
     }
   }
 
-  // O^T += V^T P^T over half a page
+  // O^T += V^T P^T over half a page.  value(d): the operand of dimension
+  // 16 d + c16, tokens 16 t + 4 g + r of the half's two tiles t.
   template <typename Value>
-  __device__ __forceinline__ void accumulate(const Value& value, const half8 (&p)[RT], int half) {
+  __device__ __forceinline__ void accumulate(const Value& value, const half8 (&p)[RT]) {
 #pragma unroll
     for (int d = 0; d < DT; ++d) {
-      const u32x4 v = value(d);
-      const half8 vf = decode_e4m3x8(v[2 * half], v[2 * half + 1]);
+      const half8 vf = value(d);
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) o[d][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[rt], o[d][rt], 0, 0, 0);
     }
   }
-
-  // The same with the values times `factor`, and with codes of tokens that no
-  // row of the wavefront sees as zeros (what is there may be anything); a NaN
-  // code that some rows see and others do not is taken out too, and put into
-  // the rows that see it.
-  template <typename Value>
-  __device__ __forceinline__ void accumulate_edge(const Value& value, const half8 (&p)[RT], int half, float factor,
-                                                  int base, int g, const View<RT>& see) {
-    const uint32_t some = seen_of(see.lim_max, see.low_min, base, g);
-    uint32_t keep[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) keep[t] = ((((some >> (16 * t)) & 15u) * 0x00204081u) & 0x01010101u) * 255u;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const u32x4 both = value(d);
-      uint32_t v[2], n[2];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        v[t] = both[2 * half + t] & keep[t];
-        n[t] = nan_bytes(v[t]) >> 7;  // 1 in NaN bytes
-      }
-      if (__ballot((n[0] | n[1]) != 0)) {
-        const half8 f = decode_e4m3x8(n[0] * 0x38u, n[1] * 0x38u);  // 1.0 there
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          const uint32_t seen = seen_of(see.lim[rt], see.low[rt], base, g);
-          u32x4 sees;  // FP16 1 where the row sees the token
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            sees[e] = (all_ones_if(seen, e >> 1, 2 * (e & 1)) & 0x3C00u) |
-                      (all_ones_if(seen, e >> 1, 2 * (e & 1) + 1) & 0x3C000000u);
-          const float4v hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(f, __builtin_bit_cast(half8, sees), float4v{0, 0, 0, 0},
-                                                                    0, 0, 0);
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            if (hit[r] > 0.0f) o[d][rt][r] = __builtin_nanf("");
-        }
-        v[0] &= ~(n[0] * 255u);
-        v[1] &= ~(n[1] * 255u);
-      }
-      const half8 vf = decode_e4m3x8(v[0], v[1]);
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const float4v add = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[rt], float4v{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) o[d][rt][r] = __builtin_fmaf(add[r], factor, o[d][rt][r]);
-        // here, not behind the last tile, where every product would still be held
-        asm volatile("" : "+v"(o[d][rt]));
-      }
-    }
-  }
 };
 
-// The blocks and scales of up to 64 pages of a request, one a lane: entries
+// NaN into the sums o of the rows that see it; nan: FP16 ones where a value is
+// NaN, zeros elsewhere; seen: the tokens of the half page that the row sees.
+__device__ __forceinline__ void spread_nan(const half8& nan, uint32_t seen, float4v& o) {
+  u32x4 sees;  // FP16 1 where the row sees the token
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    sees[e] = (all_ones_if(seen, e >> 1, 2 * (e & 1)) & 0x3C00u) |
+              (all_ones_if(seen, e >> 1, 2 * (e & 1) + 1) & 0x3C000000u);
+  const float4v hit = __builtin_amdgcn_mfma_f32_16x16x32_f16(nan, __builtin_bit_cast(half8, sees), float4v{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (hit[r] > 0.0f) o[r] = __builtin_nanf("");
+  // one product at a time: this is rare, and its registers are the loop's
+  asm volatile("" : "+v"(o));
+}
+
+// Workgroup barrier that waits for this wavefront's LDS accesses alone: loads
+// of pages stay in flight across it.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// All bits of the bytes (of the FP16 values) of tokens that are seen: a word
+// for each tile t of a half page (for each pair of tokens).
+__device__ __forceinline__ uint32_t keep_bytes(uint32_t seen, int t) {
+  return ((((seen >> (16 * t)) & 15u) * 0x00204081u) & 0x01010101u) * 255u;
+}
+__device__ __forceinline__ u32x4 keep_halves(uint32_t seen) {
+  u32x4 k;
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    k[e] = (all_ones_if(seen, e >> 1, 2 * (e & 1)) & 0xFFFFu) | (all_ones_if(seen, e >> 1, 2 * (e & 1) + 1) & 0xFFFF0000u);
+  return k;
+}
+
+// Values of a page that some rows see only a part of, codes of the D tiles of a
+// wavefront: what no row sees becomes zeros (what is there may be anything); NaN
+// that some rows see and others do not is taken out too, and put into the sums
+// of the rows that see it.
+template <int D, int RT>
+__device__ __forceinline__ void clean_values(u32x4 (&v)[D], int base, int g, const View<RT>& see, float4v (&o)[D][RT]) {
+  uint32_t any = 0;
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t keep = keep_bytes(seen_of(see.lim_max, see.low_min, base + 32 * (t >> 1), g), t & 1);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const uint32_t x = v[d][t] & keep;
+      v[d][t] = x;
+      any |= nan_bytes(x);
+    }
+  }
+  if (__builtin_expect(__ballot(any != 0) == 0, 1)) return;
+#pragma unroll
+  for (int half = 0; half < 2; ++half)
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const uint32_t n0 = nan_bytes(v[d][2 * half]) >> 7, n1 = nan_bytes(v[d][2 * half + 1]) >> 7;
+      const half8 nan = decode_e4m3x8(n0 * 0x38u, n1 * 0x38u);  // E4M3 ones
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) spread_nan(nan, seen_of(see.lim[rt], see.low(rt), base + 32 * half, g), o[d][rt]);
+      v[d][2 * half] &= ~(n0 * 255u);
+      v[d][2 * half + 1] &= ~(n1 * 255u);
+    }
+}
+
+// The numbers and scales of up to 64 pages of a request, one a lane: entries
 // first + lane * step below end.
 struct Pages {
-  int64_t block;
+  int id;  // 0 (with a NaN factor) for one that is not in the cache
   float kc, vs;
   __device__ __forceinline__ void load(const AttentionArgs& a, const int32_t* table, int head, bool bad, int lane,
                                        int first, int step, int end) {
     const int page = first + lane * step;  // (both below 2^25)
-    block = head;
+    id = 0;
     kc = __builtin_nanf("");
     vs = 1.0f;
     if (page < end && page < a.table_width) {
-      const int32_t id = table[page];
-      if (id >= 0 && id < a.cache.pages && !bad) {
-        block = (int64_t)id * a.cache.heads + head;
+      const int32_t x = table[page];
+      if (x >= 0 && x < a.cache.pages && !bad) {
+        const int64_t block = (int64_t)x * a.cache.heads + head;
+        id = x;
         kc = a.cache.k_scale[block] * (a.scale * 1.44269504088896340736f);
         vs = a.cache.v_scale[block];
       }
     }
   }
-  __device__ __forceinline__ int64_t block_at(int i) const {
-    const int lo = __builtin_amdgcn_readlane((int)(block & 0xFFFFFFFF), i);
-    const int hi = __builtin_amdgcn_readlane((int)(block >> 32), i);
-    return ((int64_t)hi << 32) | (uint32_t)lo;
+  // byte offset of the page's block
+  template <int DIM>
+  __device__ __forceinline__ int64_t offset_at(const AttentionArgs& a, int head, int i) const {
+    return ((int64_t)__builtin_amdgcn_readlane(id, i) * a.cache.heads + head) * (kKvPage * DIM);
   }
   static __device__ __forceinline__ float at(float x, int i) {
     return __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), i));
@@ -516,11 +515,10 @@ __device__ __forceinline__ View<RT> view_of(const AttentionArgs& a, int group, c
                                             int rows) {
   const int c16 = lane & 15, at = q.seq - q.rows + 1;
   View<RT> v;
+  v.window = a.window;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
+  for (int t = 0; t < RT; ++t)
     v.lim[t] = t * 16 + c16 < rows ? at + (int)((uint32_t)(first + t * 16 + c16) / (uint32_t)group) : 0;
-    v.low[t] = a.window > 0 ? max(0, v.lim[t] - a.window) : 0;
-  }
   v.lim_min = uniform(at + (int)((uint32_t)first / (uint32_t)group));
   v.lim_max = uniform(at + (int)((uint32_t)(first + rows - 1) / (uint32_t)group));
   v.low_min = a.window > 0 ? max(0, v.lim_min - a.window) : 0;
@@ -597,15 +595,67 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, int n, uint32_t* 
   return last;
 }
 
+// Joins F fragments (f0 on, of one row tile) of `count` partial sums in order.
+// slot(i): the i-th one's slot.  All loads of kJoinChunk sums go out together.
+template <int DIM, int TILES, int F, typename SlotOf>
+__device__ __forceinline__ void join_fragments(__amdgpu_buffer_rsrc_t res, int lane, int f0, int count,
+                                               const SlotOf& slot, float4v (&sum)[F], float& top, float& weight) {
+  using S = Slot<DIM, TILES>;
+  constexpr int CH = F > 2 ? 4 : 8;
+  const int rt = f0 / S::DT, d0 = f0 % S::DT, c16 = lane & 15;
+  top = kLowest, weight = 0.0f;
+#pragma unroll
+  for (int f = 0; f < F; ++f) sum[f] = float4v{0, 0, 0, 0};
+#pragma unroll 1
+  for (int i0 = 0; i0 < count; i0 += CH) {
+    float4v o[CH][F];
+    float2v ml[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      const int at = slot(min(i0 + i, count - 1)) * S::kBytes;
+      ml[i] = __builtin_bit_cast(float2v, __builtin_amdgcn_raw_buffer_load_b64(res, S::row(rt, c16), at, kDevScope));
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+        o[i][f] = __builtin_bit_cast(
+            float4v, __builtin_amdgcn_raw_buffer_load_b128(res, S::fragment(rt, d0 + f, lane), at, kDevScope));
+    }
+    float up = top;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) up = fmaxf(up, ml[i][0]);
+    const float old = __builtin_amdgcn_exp2f(top - up);
+    top = up;
+    weight *= old;
+#pragma unroll
+    for (int f = 0; f < F; ++f) sum[f] *= old;
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+      if (i0 + i < count) {
+        const float w = __builtin_amdgcn_exp2f(ml[i][0] - top);
+        weight += ml[i][1] * w;
+#pragma unroll
+        for (int f = 0; f < F; ++f) sum[f] += o[i][f] * w;
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t partial_of(const AttnLaunch& l) {
+  return __builtin_amdgcn_make_buffer_rsrc((void*)l.partial, (short)0, 0x7FFFFFFF, kRsrc);
+}
+
 // After the pieces' sums are stored: the last workgroup of a segment (of a
 // group of its pieces first, when there are many) joins them in order and
-// writes y.  Fragments go to the wavefronts in turn.
+// writes y.  Each wavefront takes a share of the fragments.
 template <int DIM, int TILES, int WAVES>
 __device__ __forceinline__ void join_pieces(const AttentionArgs& a, const AttnLaunch& l, const Item& it, const Req& q,
                                             int lane, int wave, int row_first, int rows_here, uint32_t* s_arrival) {
   using S = Slot<DIM, TILES>;
+  constexpr int PER = TILES * S::DT / WAVES;  // fragments of a wavefront
+  constexpr int F = PER >= 4 ? 4 : PER >= 2 ? 2 : 1;
+  constexpr int SHARES = TILES * S::DT / F;
+  static_assert(S::DT % F == 0 && SHARES * F == TILES * S::DT, "a share lies in one row tile");
   const int c16 = lane & 15, g = lane >> 4;
-  const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc((void*)l.partial, (short)0, 0x7FFFFFFF, kRsrc);
+  const __amdgpu_buffer_rsrc_t res = partial_of(l);
   uint32_t* const counters = (uint32_t*)a.scratch;
   // groups of pieces: one when all are joined directly, else about the root
   // of their number; group k has pieces k n / groups .. (k + 1) n / groups - 1
@@ -620,73 +670,71 @@ __device__ __forceinline__ void join_pieces(const AttentionArgs& a, const AttnLa
   if (!arrive_last(counters + (it.first + p0) * kCounterStep, p1 - p0, s_arrival)) return;
   // slots of groups lie behind those of pieces; a group has two pieces or
   // more, so half its first piece's number is a slot of its own
-  int count = p1 - p0, first = it.first + p0;
-  bool inner = groups > 1;
+  int count = p1 - p0;
+  const int first = it.first + p0;
+  bool inner = groups > 1, outer = false;
   for (;;) {
-    auto slot_of = [&](int i) {
-      return inner || groups == 1 ? first + i : l.slots + (it.first + start_of(i)) / 2;
-    };
-    for (int f = wave; f < TILES * S::DT; f += WAVES) {
-      const int rt = f / S::DT, d = f % S::DT;
+    auto slot = [&](int i) { return outer ? l.slots + (it.first + start_of(i)) / 2 : first + i; };
+#pragma unroll 1
+    for (int share = wave; share < SHARES; share += WAVES) {
+      const int f0 = share * F, rt = f0 / S::DT, d0 = f0 % S::DT;
       if (rt * 16 >= rows_here) break;
-      float4v sum{0, 0, 0, 0};
-      float top = kLowest, weight = 0.0f;
-      for (int i0 = 0; i0 < count; i0 += kJoinDirect) {
-        float4v o[kJoinDirect];
-        float2v ml[kJoinDirect];
-#pragma unroll
-        for (int i = 0; i < kJoinDirect; ++i) {
-          const int at = slot_of(min(i0 + i, count - 1)) * S::kBytes;
-          ml[i] = __builtin_bit_cast(float2v, __builtin_amdgcn_raw_buffer_load_b64(res, at + S::row(rt, c16), 0, kDevScope));
-          o[i] = __builtin_bit_cast(float4v, __builtin_amdgcn_raw_buffer_load_b128(res, at + S::fragment(rt, d, lane), 0, kDevScope));
-        }
-        float up = top;
-#pragma unroll
-        for (int i = 0; i < kJoinDirect; ++i) up = fmaxf(up, ml[i][0]);
-        const float old = __builtin_amdgcn_exp2f(top - up);
-        top = up;
-        sum *= old;
-        weight *= old;
-#pragma unroll
-        for (int i = 0; i < kJoinDirect; ++i) {
-          const float f = i0 + i < count ? __builtin_amdgcn_exp2f(ml[i][0] - top) : 0.0f;
-          if (i0 + i < count) {
-            sum += o[i] * f;
-            weight += ml[i][1] * f;
-          }
-        }
-      }
+      float4v sum[F];
+      float top, weight;
+      join_fragments<DIM, TILES, F>(res, lane, f0, count, slot, sum, top, weight);
       if (inner) {
         const int at = (l.slots + first / 2) * S::kBytes;
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum), res, at + S::fragment(rt, d, lane), 0, kDevScope);
-        if (d == 0 && g == 0)
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, float2v{top, weight}), res, at + S::row(rt, c16),
-                                                0, kDevScope);
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum[f]), res, S::fragment(rt, d0 + f, lane), at,
+                                                 kDevScope);
+        if (d0 == 0 && g == 0)
+          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, float2v{top, weight}), res, S::row(rt, c16), at,
+                                                kDevScope);
       } else if (rt * 16 + c16 < rows_here) {
-        write_y(a, l.group, q, it.head, row_first + rt * 16 + c16, 16 * d + 4 * g, DIM, sum, weight);
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+          write_y(a, l.group, q, it.head, row_first + rt * 16 + c16, 16 * (d0 + f) + 4 * g, DIM, sum[f], weight);
       }
     }
     if (!inner) return;
     if (!arrive_last(counters + (kMaxPieces + it.first) * kCounterStep, groups, s_arrival)) return;
     inner = false;
+    outer = true;
     count = groups;
   }
 }
 
 // ---------------------------------------------------------------------------
-// Few rows: a wavefront takes whole pages.
+// Few rows: the workgroup takes a page per wavefront at a time.
+//
+// First product: wavefront w computes the weights of page w of these, all rows,
+// against a running maximum of its own (a row's pages need not agree on one),
+// and leaves them in LDS as the operands of the second product.  Second product:
+// wavefront w takes the 16 dimensions w of all the pages; a page's sums are added
+// with the factor exp2(its maximum - the common one) times its V scale.  So every
+// code is converted once, no wavefront holds more than its dimensions' sums, and
+// nothing is left to join but the weights' sums.  Two buffers: one barrier for W
+// pages.  The next keys are on their way once this page's are used, the next
+// values of a page once its present ones are.
 // ---------------------------------------------------------------------------
 template <int DIM, int RT>
-__global__ __launch_bounds__(few_waves(DIM, RT) * 64) void attention_few_kernel(AttentionArgs a, AttnLaunch l) {
-  using R = Rows<DIM, RT>;
+struct FewLds {
+  static constexpr int W = few_waves(DIM), KS = DIM / 32, ROWS = 16 * RT;
+  half8 p[2][W][2][RT][64];  // operands of the second product: page, k-step, row tile, lane
+  half8 q[KS][RT][64];       // operands of the first
+  float m[2][ROWS][W];       // the pages' maxima
+  float last[W][ROWS], sum[W][ROWS];
+};
+
+template <int DIM, int RT>
+__global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(AttentionArgs a, AttnLaunch l) {
   using S = Slot<DIM, RT>;
-  constexpr int W = few_waves(DIM, RT);
-  constexpr int DT = R::DT, KS = R::KS, ROWS = 16 * RT;
-  constexpr bool kQueryLds = RT > 1;  // the queries' fragments are read from LDS for each page
-  __shared__ float s_m[W][ROWS], s_l[W][ROWS];
-  __shared__ __attribute__((aligned(16))) half8 s_q[kQueryLds ? KS * RT * 64 : 1];
+  using L = FewLds<DIM, RT>;
+  constexpr int W = L::W, KS = L::KS, ROWS = L::ROWS, DW = DIM / 16 / W;  // dimension tiles of a wavefront
   __shared__ uint32_t s_arrival;
-  extern __shared__ __attribute__((aligned(16))) float s_o[];  // [W][DT][64][4]
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_few[];
+  L& s = *reinterpret_cast<L*>(s_few);
   const int wave = uniform((int)threadIdx.x >> 6);
 
   for (int block = blockIdx.x;; block += gridDim.x) {
@@ -700,148 +748,269 @@ __global__ __launch_bounds__(few_waves(DIM, RT) * 64) void attention_few_kernel(
     const int row_first = it.tile * ROWS;  // among the segment's rows
     const int rows_here = min(ROWS, q.rows * l.group - row_first);
     const View<RT> see = view_of<RT>(a, l.group, q, lane, row_first, rows_here);
-    // the piece's pages that the tile sees; this wavefront takes every
-    // W-th
-    const int lo = max(q.first_page + (int)((int64_t)q.pages * it.piece / it.pieces), see.low_min / kKvPage) + wave;
+    // the piece's pages that the tile sees
+    const int lo = max(q.first_page + (int)((int64_t)q.pages * it.piece / it.pieces), see.low_min / kKvPage);
     const int hi = min(q.first_page + (int)((int64_t)q.pages * (it.piece + 1) / it.pieces),
                        (see.lim_max + kKvPage - 1) / kKvPage);
+    const int count = max(0, hi - lo);
     const int32_t* const table = a.table + it.request * a.table_stride;
-    Pages pages;
-    pages.load(a, table, it.head, q.bad, lane, lo, W, hi);
+    Pages now;  // of the 64 pages around the present ones
+    now.load(a, table, it.head, q.bad, lane, lo, 1, hi);
 
-    u32x4 k[DIM / 64][4], v[DT];
+    u32x4 k[DIM / 64][4], v[W][DW];
     const int k_at = g * (kKvPage * 16) + c16 * 16, v_at = c16 * kKvPage + 16 * g;
-    auto load_keys = [&](int64_t block) {
+    auto load_keys = [&](int64_t offset) {
       const __amdgpu_buffer_rsrc_t res =
-          __builtin_amdgcn_make_buffer_rsrc((void*)(a.cache.k + block * (kKvPage * DIM)), (short)0, kKvPage * DIM, kRsrc);
+          __builtin_amdgcn_make_buffer_rsrc((void*)(a.cache.k + offset), (short)0, kKvPage * DIM, kRsrc);
 #pragma unroll
       for (int u = 0; u < DIM / 64; ++u)
 #pragma unroll
         for (int t = 0; t < 4; ++t)
           k[u][t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(res, k_at + t * 256, u * 4 * kKvPage * 16, 0));
     };
-    auto load_values = [&](int64_t block) {
+    auto load_values = [&](int64_t offset, u32x4(&to)[DW]) {
       const __amdgpu_buffer_rsrc_t res =
-          __builtin_amdgcn_make_buffer_rsrc((void*)(a.cache.v + block * (kKvPage * DIM)), (short)0, kKvPage * DIM, kRsrc);
+          __builtin_amdgcn_make_buffer_rsrc((void*)(a.cache.v + offset), (short)0, kKvPage * DIM, kRsrc);
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-        v[d] = __builtin_bit_cast(
-            u32x4, __builtin_amdgcn_raw_buffer_load_b128(res, v_at + d % 4 * (16 * kKvPage), d / 4 * 64 * kKvPage, 0));
+      for (int d = 0; d < DW; ++d)
+        to[d] = __builtin_bit_cast(
+            u32x4, __builtin_amdgcn_raw_buffer_load_b128(res, v_at, (wave * DW + d) * (16 * kKvPage), 0));
     };
-    if (lo < hi) {
-      const int64_t first = pages.block_at(0);
-      load_keys(first);
-      load_values(first);
-    }
-    half8 qr[KS];
-    if constexpr (kQueryLds) {
-      if (wave < RT) {
-        load_query<DIM>(a, l.group, q, it.head, lane, row_first, rows_here, wave, qr);
+    if (count > 0) {
+      load_keys(now.template offset_at<DIM>(a, it.head, min(wave, count - 1)));
 #pragma unroll
-        for (int i = 0; i < KS; ++i) s_q[(i * RT + wave) * 64 + lane] = qr[i];
-      }
-      __syncthreads();
-    } else {
-      load_query<DIM>(a, l.group, q, it.head, lane, row_first, rows_here, 0, qr);
+      for (int j = 0; j < W; ++j) load_values(now.template offset_at<DIM>(a, it.head, min(j, count - 1)), v[j]);
     }
-    auto query = [&](int i, int rt) { return kQueryLds ? s_q[(i * RT + rt) * 64 + lane] : qr[i]; };
-    R rows;
-    rows.begin(Pages::at(pages.vs, 0));
-    const int count = lo < hi ? (hi - lo + W - 1) / W : 0;
-    // Page i with the next page's keys (the last one's again at the end) on
-    // their way once its own are used, the next values behind its own.
-    const auto key = [&](int u, int t) { return k[u][t]; };
-    const auto value = [&](int d) { return v[d]; };
-    int i = 0;
-    float kc = 0.0f, vs = 0.0f;
-    int64_t next = 0;
-    const auto turn_to = [&]() {  // page i's factors, the next page's block
-      kc = Pages::at(pages.kc, i & 63), vs = Pages::at(pages.vs, i & 63);
-      if ((i & 63) == 63 && i + 1 < count)
-        pages.load(a, table, it.head, q.bad, lane, lo + (i + 1) * W, W, hi);
-      next = pages.block_at(i + 1 < count ? (i + 1) & 63 : i & 63);
-    };
-    const auto fetch = [&] { load_keys(next); };
-    if (count > 0) turn_to();
-    while (i < count) {
-      // the loop over ordinary pages by itself, which keeps the sums in place
-      while (rows.ordinary(kc, vs, (lo + i * W) * kKvPage, see)) {
-        rows.template page<false>(key, query, value, fetch, kc, vs, 0, g, see);
-        load_values(next);
-        if (++i == count) break;
-        turn_to();
-      }
-      if (i < count) {
-        rows.template page<true>(key, query, value, fetch, kc, vs, (lo + i * W) * kKvPage, g, see);
-        load_values(next);
-        if (++i < count) turn_to();
-      }
+    for (int t = wave; t < RT; t += W) {
+      half8 qr[KS];
+      load_query<DIM>(a, l.group, q, it.head, lane, row_first, rows_here, t, qr);
+#pragma unroll
+      for (int i = 0; i < KS; ++i) s.q[i][t][lane] = qr[i];
     }
+    lds_barrier();
 
-    // join the wavefronts: a common maximum per row, then the sums in order
+    float m[RT], sum[RT], top[RT];  // this wavefront's maxima and sums, the common maximum
+    float4v o[DW][RT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      rows.sum[rt] += __shfl_xor(rows.sum[rt], 16);
-      rows.sum[rt] += __shfl_xor(rows.sum[rt], 32);
-      if (g == 0) s_m[wave][rt * 16 + c16] = rows.m[rt], s_l[wave][rt * 16 + c16] = rows.sum[rt];
+      m[rt] = top[rt] = kLowest;
+      sum[rt] = 0.0f;
+#pragma unroll
+      for (int d = 0; d < DW; ++d) o[d][rt] = float4v{0, 0, 0, 0};
     }
-    __syncthreads();
-    const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc((void*)l.partial, (short)0, 0x7FFFFFFF, kRsrc);
+
+    for (int i0 = 0; i0 < count; i0 += W) {
+      const int buffer = (i0 / W) & 1, at = i0 & 63;  // (64 is a multiple of W)
+      const int here = min(W, count - i0), left = count - i0 - W;  // pages of this step, behind it
+      Pages next = now;  // the next step's pages: lanes (at + W) & 63 on
+      if (at + W == 64 && left > 0) next.load(a, table, it.head, q.bad, lane, lo + i0 + W, 1, hi);
+      const int next_at = left > 0 ? (at + W) & 63 : at, last = left > 0 ? min(W, left) - 1 : here - 1;
+      if (wave < here) {
+        // the weights of page i0 + wave
+        float kc = Pages::at(now.kc, at + wave);
+        const int base = (lo + i0 + wave) * kKvPage;
+        float4v x[4][RT];
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) x[t][rt] = float4v{0, 0, 0, 0};
+#pragma unroll
+        for (int u = 0; u < DIM / 64; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            half8 qf[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) qf[rt] = s.q[2 * u + h][rt][lane];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+              const half8 kf = decode_e4m3x8(k[u][t][2 * h], k[u][t][2 * h + 1]);
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt)
+                x[t][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[rt], x[t][rt], 0, 0, 0);
+            }
+          }
+        load_keys(next.template offset_at<DIM>(a, it.head, next_at + min(wave, last)));
+        if (base + kKvPage > see.lim_min || base < see.low_max || !(kc > 0.0f)) {
+          // a negative factor moves to the scores; for 0 any does, with zeros;
+          // what a row does not see is -inf
+          float sign = 1.0f;
+          if (!(kc > 0.0f)) {
+            sign = kc == 0.0f ? 0.0f : -1.0f;
+            kc = kc == 0.0f ? 1.0f : -kc;
+          }
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const uint32_t seen = seen_of(see.lim[rt], see.low(rt), base + 32 * half, g);
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                  const uint32_t ones = all_ones_if(seen, t, r);
+                  const float z = x[2 * half + t][rt][r] * sign;
+                  x[2 * half + t][rt][r] =
+                      __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, z) & ones) | (0xFF800000u & ~ones));
+                }
+            }
+        }
+        float high[RT];
+        bool raise = false;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          float mx = fmaxf(x[0][rt][0], x[0][rt][1]);
+#pragma unroll
+          for (int i = 2; i < 16; i += 2) mx = fmaxf(fmaxf(mx, x[i >> 2][rt][i & 3]), x[i >> 2][rt][(i & 3) + 1]);
+          high[rt] = mx * kc;
+          raise |= high[rt] > m[rt] + kMaxSlack;
+        }
+        if (__ballot(raise)) {
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            float mx = fmaxf(high[rt], __shfl_xor(high[rt], 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            const float up = fmaxf(m[rt], mx);
+            sum[rt] *= __builtin_amdgcn_exp2f(m[rt] - up);
+            m[rt] = up;
+          }
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][rt][r], kc, -m[rt]));
+              part[t] += w;
+              x[t][rt][r] = w;
+            }
+          sum[rt] += (part[0] + part[1]) + (part[2] + part[3]);
+          s.p[buffer][wave][0][rt][lane] = to_half8(x[0][rt], x[1][rt]);
+          s.p[buffer][wave][1][rt][lane] = to_half8(x[2][rt], x[3][rt]);
+          if (g == 0) s.m[buffer][rt * 16 + c16][wave] = m[rt];
+        }
+      }
+      lds_barrier();
+
+      // the common maximum and the pages' factors
+      float f[W][RT];
+      bool grown = false;
+      float up[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        up[rt] = top[rt];
+#pragma unroll
+        for (int j = 0; j < W; j += 4) {
+          const float4v mj = *reinterpret_cast<const float4v*>(&s.m[buffer][rt * 16 + c16][j]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            f[j + e][rt] = mj[e];
+            if (j + e < here) up[rt] = fmaxf(up[rt], mj[e]);
+          }
+        }
+        grown |= up[rt] > top[rt];
+      }
+      if (__ballot(grown)) {
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          const float scale = __builtin_amdgcn_exp2f(top[rt] - up[rt]);
+          top[rt] = up[rt];
+#pragma unroll
+          for (int d = 0; d < DW; ++d) o[d][rt] *= scale;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        if (j < here) {
+          const int base = (lo + i0 + j) * kKvPage;
+          const float vs = Pages::at(now.vs, at + j);
+          half8 pf[2][RT];
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) pf[h][rt] = s.p[buffer][j][h][rt][lane];
+          if (base + kKvPage > see.lim_min || base < see.low_max)
+            clean_values<DW, RT>(v[j], base, g, see, o);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) f[j][rt] = __builtin_amdgcn_exp2f(f[j][rt] - top[rt]) * vs;
+#pragma unroll
+          for (int d = 0; d < DW; ++d) {
+            half8 vf[2];
+            decode_fp8_fragment(v[j][d], vf);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+              float4v add{0, 0, 0, 0};
+#pragma unroll
+              for (int h = 0; h < 2; ++h) add = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[h], pf[h][rt], add, 0, 0, 0);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) o[d][rt][r] = __builtin_fmaf(add[r], f[j][rt], o[d][rt][r]);
+            }
+          }
+          load_values(next.template offset_at<DIM>(a, it.head, next_at + min(j, last)), v[j]);
+        }
+      }
+      now = next;
+    }
+
+    // the weights' sums of all pages against the common maximum
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      sum[rt] += __shfl_xor(sum[rt], 16);
+      sum[rt] += __shfl_xor(sum[rt], 32);
+      if (g == 0) s.last[wave][rt * 16 + c16] = m[rt], s.sum[wave][rt * 16 + c16] = sum[rt];
+      sum[rt] = 0.0f;
+    }
+    lds_barrier();
+#pragma unroll 1
+    for (int w = 0; w < W; ++w) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        sum[rt] += s.sum[w][rt * 16 + c16] * __builtin_amdgcn_exp2f(s.last[w][rt * 16 + c16] - top[rt]);
+    }
+    const __amdgpu_buffer_rsrc_t res = partial_of(l);
     const int slot = (it.first + it.piece) * S::kBytes;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       if (rt * 16 >= rows_here) break;
-      const int row = rt * 16 + c16;
-      float top = s_m[0][row];
 #pragma unroll
-      for (int w = 1; w < W; ++w) top = fmaxf(top, s_m[w][row]);
-      float weight = 0.0f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) weight += s_l[w][row] * __builtin_amdgcn_exp2f(s_m[w][row] - top);
-      const float f = __builtin_amdgcn_exp2f(rows.m[rt] - top) * rows.vref;
-      if (rt > 0) __syncthreads();  // the previous tile's sums have been read
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-        *reinterpret_cast<float4v*>(s_o + ((wave * DT + d) * 64 + lane) * 4) = rows.o[d][rt] * f;
-      __syncthreads();
-#pragma unroll
-      for (int d = wave; d < DT; d += W) {
-        float4v sum = *reinterpret_cast<const float4v*>(s_o + (d * 64 + lane) * 4);
-#pragma unroll
-        for (int w = 1; w < W; ++w) sum += *reinterpret_cast<const float4v*>(s_o + ((w * DT + d) * 64 + lane) * 4);
+      for (int d = 0; d < DW; ++d) {
         if (it.pieces == 1) {
-          if (row < rows_here) write_y(a, l.group, q, it.head, row_first + row, 16 * d + 4 * g, DIM, sum, weight);
+          if (rt * 16 + c16 < rows_here)
+            write_y(a, l.group, q, it.head, row_first + rt * 16 + c16, 16 * (wave * DW + d) + 4 * g, DIM, o[d][rt], sum[rt]);
         } else {
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum), res, slot + S::fragment(rt, d, lane), 0, kDevScope);
-          if (d == 0 && g == 0)
-            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, float2v{top, weight}), res,
-                                                  slot + S::row(rt, c16), 0, kDevScope);
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[d][rt]), res,
+                                                 S::fragment(rt, wave * DW + d, lane), slot, kDevScope);
         }
       }
+      if (it.pieces > 1 && wave == 0 && g == 0)
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, float2v{top[rt], sum[rt]}), res, S::row(rt, c16),
+                                              slot, kDevScope);
     }
     if (it.pieces > 1) join_pieces<DIM, RT, W>(a, l, it, q, lane, wave, row_first, rows_here, &s_arrival);
-    __syncthreads();  // LDS is free for the next item
+    lds_barrier();  // LDS is free for the next item
   }
 }
 
 // ---------------------------------------------------------------------------
 // Many rows: a workgroup's wavefronts share each page through LDS.
 //
-// Two buffers of a page: while one is used, the next page is on its way into
-// registers, and it goes to the other buffer behind the arithmetic, so there
-// is one barrier a page.  16-byte units of values are stored turned by
-// (dimension / 4) % 4 within their dimension's four, so that the 16 lanes
-// that read one group of 16 dimensions meet all LDS banks.
+// The workgroup converts a page to FP16 once, into the order of the products'
+// A operands (a conversion costs as much as two additions, and each wavefront
+// on its own would spend half its vector time on them).  Two buffers: while one
+// is used, the next page is on its way into registers, and it goes to the other
+// buffer behind the arithmetic, so there is one barrier a page.
 // ---------------------------------------------------------------------------
 template <int DIM, int RT>
-__global__ __launch_bounds__(kManyWaves * 64, 2) void attention_many_kernel(AttentionArgs a, AttnLaunch l) {
+__global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_many_kernel(AttentionArgs a, AttnLaunch l) {
   using R = Rows<DIM, RT>;
   using S = Slot<DIM, RT * kManyWaves>;
-  constexpr int DT = R::DT, KS = R::KS, ROWS = 16 * RT * kManyWaves, THREADS = kManyWaves * 64;
-  constexpr int UNITS = kKvPage * DIM / 16;    // 16-byte units of a block
-  constexpr int PER = UNITS / THREADS;         // of a thread
-  __shared__ __attribute__((aligned(16))) u32x4 s_k[2][UNITS], s_v[2][UNITS];
-  __shared__ uint32_t s_arrival;
+  constexpr int DT = R::DT, KS = R::KS, ROWS = 16 * RT * kManyWaves;
+  constexpr int KF = DIM / 16, VF = DIM / 16;  // 16-byte-a-lane loads of a block of keys, of values
+  constexpr int PER = KF / kManyWaves;          // of a wavefront
+  extern __shared__ __attribute__((aligned(16))) half8 s_pages[];
+  half8(*const s_k)[KF * 2 * 64] = reinterpret_cast<half8(*)[KF * 2 * 64]>(s_pages);
+  half8(*const s_v)[VF * 2 * 64] = reinterpret_cast<half8(*)[VF * 2 * 64]>(s_pages + 2 * KF * 2 * 64);
   const int wave = uniform((int)threadIdx.x >> 6);
 
   for (int block = blockIdx.x;; block += gridDim.x) {
@@ -871,25 +1040,35 @@ __global__ __launch_bounds__(kManyWaves * 64, 2) void attention_many_kernel(Atte
     R rows;
     rows.begin(Pages::at(pages.vs, 0));
 
+    // load n of the keys: unit 4 u + g of token 16 t + c16, n = 4 u + t; of the
+    // values: dimension 16 n + c16, group g
     u32x4 kr[PER], vr[PER];
-    auto load = [&](int64_t block) {
-      const u32x4* const ks = reinterpret_cast<const u32x4*>(a.cache.k + block * (kKvPage * DIM));
-      const u32x4* const vs = reinterpret_cast<const u32x4*>(a.cache.v + block * (kKvPage * DIM));
+    auto load = [&](int64_t offset) {
+      const uint8_t* const ks = a.cache.k + offset;
+      const uint8_t* const vs = a.cache.v + offset;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) kr[i] = ks[i * THREADS + tid];
+      for (int i = 0; i < PER; ++i) {
+        const int n = wave * PER + i;
+        kr[i] = *reinterpret_cast<const u32x4*>(ks + (((n >> 2) * 4 + g) * kKvPage + (n & 3) * 16 + c16) * 16);
+      }
 #pragma unroll
-      for (int i = 0; i < PER; ++i) vr[i] = vs[i * THREADS + tid];
+      for (int i = 0; i < PER; ++i)
+        vr[i] = *reinterpret_cast<const u32x4*>(vs + ((wave * PER + i) * 16 + c16) * kKvPage + 16 * g);
     };
     auto put = [&](int buffer) {
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
-        const int u = i * THREADS + tid;
-        s_k[buffer][u] = kr[i];
-        s_v[buffer][u ^ ((u >> 4) & 3)] = vr[i];
+        half8 f[2];
+        decode_fp8_fragment(kr[i], f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s_k[buffer][((wave * PER + i) * 2 + h) * 64 + lane] = f[h];
+        decode_fp8_fragment(vr[i], f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) s_v[buffer][((wave * PER + i) * 2 + h) * 64 + lane] = f[h];
       }
     };
     if (lo < hi) {
-      load(pages.block_at(0));
+      load(pages.offset_at<DIM>(a, it.head, 0));
       put(0);
     }
     int page = lo;
@@ -897,10 +1076,8 @@ __global__ __launch_bounds__(kManyWaves * 64, 2) void attention_many_kernel(Atte
     int buffer = 0;
     // Page `page` and the next one's way into the other buffer; every
     // wavefront of the workgroup goes through the same barriers.
-    const auto key = [&](int u, int t) { return s_k[buffer][(4 * u + g) * kKvPage + 16 * t + c16]; };
+    const auto key = [&](int u, int t, int h) { return s_k[buffer][((u * 4 + t) * 2 + h) * 64 + lane]; };
     const auto query = [&](int i, int rt) { return qr[rt][i]; };
-    const auto value = [&](int d) { return s_v[buffer][(16 * d + c16) * 4 + (g ^ (c16 >> 2))]; };
-    const auto none = [] {};
     const auto open = [&] {
       const int i = (page - lo) & 63;
       buffer = (page - lo) & 1;
@@ -908,27 +1085,81 @@ __global__ __launch_bounds__(kManyWaves * 64, 2) void attention_many_kernel(Atte
       __syncthreads();  // this page is in LDS, the other buffer has been read
       if (page + 1 < hi) {
         if (i == 63) pages.load(a, table, it.head, q.bad, lane, page + 1, 1, hi);
-        load(pages.block_at((i + 1) & 63));
+        load(pages.offset_at<DIM>(a, it.head, (i + 1) & 63));
       }
     };
     if (page < hi) open();
     while (page < hi) {
+      // the loop over ordinary pages by itself, which keeps the sums in place
       while (rows.ordinary(kc, vs, page * kKvPage, see)) {
-        rows.template page<false>(key, query, value, none, kc, vs, 0, g, see);
+        const float lift = __builtin_amdgcn_logf(vs / rows.vref), drop = rows.vref / vs;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          float4v s[2][RT];
+          half8 p[RT];
+          rows.scores(key, query, half, s);
+          rows.weigh(s, kc, lift, drop, p);
+          rows.accumulate([&](int d) { return s_v[buffer][(d * 2 + half) * 64 + lane]; }, p);
+        }
         if (page + 1 < hi) put(buffer ^ 1);
         if (++page == hi) break;
         open();
       }
       if (page < hi) {
         const int base = page * kKvPage;
-        if (some && base < see.lim_max && base + kKvPage > see.low_min)
-          rows.template page<true>(key, query, value, none, kc, vs, base, g, see);
+        if (some && base < see.lim_max && base + kKvPage > see.low_min) {
+          const typename R::Edge e = rows.settle(kc, vs);
+          const float lift = __builtin_amdgcn_logf(vs / rows.vref), drop = rows.vref / vs;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const int at = base + 32 * half;
+            // values that no row of the wavefront sees become zeros (what is
+            // there may be anything), and NaN that some see and others do not
+            u32x4 keep = keep_halves(seen_of(see.lim_max, see.low_min, at, g));
+            if (e.nothing) keep = u32x4{0, 0, 0, 0};
+            const auto value = [&](int d) {
+              return __builtin_bit_cast(half8, __builtin_bit_cast(u32x4, s_v[buffer][(d * 2 + half) * 64 + lane]) & keep);
+            };
+            bool any = false;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              const half8 x = value(d);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) any |= x[i] != x[i];
+            }
+            float4v s[2][RT];
+            half8 p[RT];
+            rows.scores(key, query, half, s);
+            rows.mask(s, e.sign, at, g, see);
+            rows.weigh(s, kc, lift, drop, p);
+            if (__builtin_expect(__ballot(any) != 0, 0)) {
+#pragma unroll
+              for (int d = 0; d < DT; ++d) {
+                half8 x = value(d);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = x[i] != x[i] ? (_Float16)1 : (_Float16)0;
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) spread_nan(x, seen_of(see.lim[rt], see.low(rt), at, g), rows.o[d][rt]);
+              }
+              rows.accumulate(
+                  [&](int d) {
+                    half8 x = value(d);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = x[i] != x[i] ? (_Float16)0 : x[i];
+                    return x;
+                  },
+                  p);
+            } else {
+              rows.accumulate(value, p);
+            }
+          }
+        }
         if (page + 1 < hi) put(buffer ^ 1);
         if (++page < hi) open();
       }
     }
 
-    const __amdgpu_buffer_rsrc_t res = __builtin_amdgcn_make_buffer_rsrc((void*)l.partial, (short)0, 0x7FFFFFFF, kRsrc);
+    const __amdgpu_buffer_rsrc_t res = partial_of(l);
     const int slot = (it.first + it.piece) * S::kBytes;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
@@ -943,15 +1174,45 @@ __global__ __launch_bounds__(kManyWaves * 64, 2) void attention_many_kernel(Atte
             write_y(a, l.group, q, it.head, row_first + rt * 16 + c16, 16 * d + 4 * g, DIM, sum, weight);
         } else {
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum), res,
-                                                 slot + S::fragment(wave * RT + rt, d, lane), 0, kDevScope);
+                                                 S::fragment(wave * RT + rt, d, lane), slot, 0);
         }
       }
       if (it.pieces > 1 && g == 0)
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, float2v{rows.m[rt], weight}), res,
-                                              slot + S::row(wave * RT + rt, c16), 0, kDevScope);
+                                              S::row(wave * RT + rt, c16), slot, 0);
     }
-    if (it.pieces > 1) join_pieces<DIM, RT * kManyWaves, kManyWaves>(a, l, it, q, lane, wave, tile_first, tile_rows, &s_arrival);
     __syncthreads();  // LDS is free for the next item
+  }
+}
+
+// Joins the pieces of cut segments of many rows: the workgroup of a piece
+// takes its share of the segment's fragments.  (A launch of its own: the last
+// workgroup alone would need tens of microseconds for a tile of 192 rows.)
+template <int DIM, int TILES>
+__global__ __launch_bounds__(kManyWaves * 64) void attention_join_kernel(AttentionArgs a, AttnLaunch l) {
+  using S = Slot<DIM, TILES>;
+  constexpr int F = 2, SHARES = TILES * S::DT / F;
+  const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
+  for (int block = blockIdx.x;; block += gridDim.x) {
+    Req q;
+    const Item it = item_of(a, l, lane, block, q);
+    if (it.request < 0) break;
+    if (it.pieces == 1) continue;
+    const int row_first = it.tile * 16 * TILES;
+    const int rows_here = min(16 * TILES, q.rows * l.group - row_first);
+    for (int share = it.piece * kManyWaves + wave; share < SHARES; share += it.pieces * kManyWaves) {
+      const int f0 = share * F, rt = f0 / S::DT, d0 = f0 % S::DT;
+      if (rt * 16 >= rows_here) break;
+      float4v sum[F];
+      float top, weight;
+      join_fragments<DIM, TILES, F>(partial_of(l), lane, f0, it.pieces, [&](int i) { return it.first + i; }, sum, top,
+                                    weight);
+      if (rt * 16 + c16 < rows_here) {
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+          write_y(a, l.group, q, it.head, row_first + rt * 16 + c16, 16 * (d0 + f) + 4 * g, DIM, sum[f], weight);
+      }
+    }
   }
 }
 
@@ -976,7 +1237,7 @@ size_t slot_bytes(const Form& f, int dim) { return (size_t)f.rows() * dim * 4 + 
 template <typename Kernel>
 hipError_t launch_kernel(Kernel kernel, int threads, size_t lds, const AttentionArgs& a, const AttnLaunch& l,
                          int64_t grid) {
-  if (lds > 65536) {
+  if (lds > 0) {
     const hipError_t e = hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
     if (e != hipSuccess) return e;
   }
@@ -984,21 +1245,29 @@ hipError_t launch_kernel(Kernel kernel, int threads, size_t lds, const Attention
   return hipGetLastError();
 }
 
+template <int DIM, int RT>
+hipError_t launch_many(const AttentionArgs& a, const AttnLaunch& l, int64_t grid) {
+  const hipError_t e = launch_kernel(attention_many_kernel<DIM, RT>, kManyWaves * 64, (size_t)4 * DIM / 16 * 2 * 1024, a,
+                                     l, grid);
+  if (e != hipSuccess || l.slots == 0) return e;
+  return launch_kernel(attention_join_kernel<DIM, RT * kManyWaves>, kManyWaves * 64, 0, a, l, grid);
+}
+
+template <int DIM, int RT>
+hipError_t launch_few(const AttentionArgs& a, const AttnLaunch& l, int64_t grid) {
+  return launch_kernel(attention_few_kernel<DIM, RT>, few_waves(DIM) * 64, sizeof(FewLds<DIM, RT>), a, l, grid);
+}
+
 template <int DIM>
 hipError_t launch_dim(const Form& f, const AttentionArgs& a, const AttnLaunch& l, int64_t grid) {
-  if (f.many) {
-    if (f.tiles == 1) return launch_kernel(attention_many_kernel<DIM, 1>, kManyWaves * 64, 0, a, l, grid);
-    return launch_kernel(attention_many_kernel<DIM, 2>, kManyWaves * 64, 0, a, l, grid);
-  }
-  const auto few = [&](auto kernel, int waves) {
-    return launch_kernel(kernel, waves * 64, (size_t)waves * DIM / 16 * 1024, a, l, grid);
-  };
-  if (f.tiles == 1) return few(attention_few_kernel<DIM, 1>, few_waves(DIM, 1));
-  if constexpr (DIM < 256) {
-    if (f.tiles == 2) return few(attention_few_kernel<DIM, 2>, few_waves(DIM, 2));
-    return few(attention_few_kernel<DIM, 3>, few_waves(DIM, 3));
-  }
-  return hipErrorInvalidValue;
+  if (!f.many)
+    return f.tiles == 1   ? launch_few<DIM, 1>(a, l, grid)
+           : f.tiles == 2 ? launch_few<DIM, 2>(a, l, grid)
+                          : launch_few<DIM, 3>(a, l, grid);
+  if (f.tiles == 1) return launch_many<DIM, 1>(a, l, grid);
+  if constexpr (DIM < 256)
+    if (f.tiles == 3) return launch_many<DIM, 3>(a, l, grid);
+  return launch_many<DIM, 2>(a, l, grid);
 }
 
 }  // namespace
