@@ -56,7 +56,8 @@ static_assert((size_t)kMaxPieces * 2 * kCounterStep * 4 <= kKvZeroedBytes, "two 
 
 // The form and the 16-row tiles of a wavefront (of a workgroup, few rows) for
 // `rows` rows of a KV head (query rows x group).
-constexpr int kFewTiles = 3;
+constexpr int few_tiles(int dim) { return dim == 256 ? 1 : 3; }   // what the registers hold
+constexpr int many_tiles(int dim) { return dim == 256 ? 1 : 3; }
 struct Form {
   bool many;
   int tiles;
@@ -64,17 +65,25 @@ struct Form {
 };
 inline Form form_for(int64_t rows, int dim) {
   const int64_t t = (rows + 15) / 16;
-  if (t <= kFewTiles) return {false, t < 1 ? 1 : (int)t};
-  return {true, t <= kManyWaves ? 1 : t <= 2 * kManyWaves || dim == 256 ? 2 : 3};
+  if (t <= few_tiles(dim)) return {false, t < 1 ? 1 : (int)t};
+  const int each = (int)((t + kManyWaves - 1) / kManyWaves < 3 ? (t + kManyWaves - 1) / kManyWaves : 3);
+  return {true, each < many_tiles(dim) ? each : many_tiles(dim)};
 }
 
 struct AttnLaunch {
   int tile_rows;   // rows of a workgroup's segment
   int group;       // query heads of a KV head
+  uint32_t inverse;  // ceil(2^32 / group), for row_of
   int target;      // pieces the lengths are cut into
   int slots;       // pieces the scratch has room for (0: segments stay whole)
   float* partial;  // 1.5 slots of partial sums (layout at Slot)
 };
+
+// The query row of row `rr` of a segment, rr / group: exact for rr < 2^26, as
+// the inverse is less than group <= 64 parts in 2^32 too large.
+__device__ __forceinline__ int row_of(const AttnLaunch& l, int rr) {
+  return l.group == 1 ? rr : (int)__umulhi((uint32_t)rr, l.inverse);
+}
 
 // One request as the kernels see it.
 struct Req {
@@ -279,19 +288,17 @@ struct Rows {
     }
   }
 
-  // Whether every row sees all of the page, whose scales are positive and in
-  // proportion.  (Uniform over the wavefront.)
-  __device__ __forceinline__ bool ordinary(float kc, float vs, int base, const View<RT>& see) const {
-    return base + kKvPage <= see.lim_min && base >= see.low_max && kc > 0.0f && vs <= vref * kScaleSlack &&
-           vs >= vref * kScaleLeast;
+  // Whether a page's scales are positive and in proportion.  (Uniform.)
+  __device__ __forceinline__ bool ordinary(float kc, float vs) const {
+    return kc > 0.0f && vs <= vref * kScaleSlack && vs >= vref * kScaleLeast;
   }
 
-  // What a page that is not an ordinary one needs beside masks.
+  // What other scales need.
   struct Edge {
     float sign;     // of the scores
     bool nothing;   // the values count for nothing
   };
-  // Takes the scales of such a page to ordinary ones.
+  // Takes such scales to ordinary ones.
   __device__ __forceinline__ Edge settle(float& kc, float& vs) {
     Edge e{1.0f, false};
     if (!(kc > 0.0f)) {  // a negative factor moves to the scores; for 0 any does, with zeros
@@ -339,7 +346,7 @@ struct Rows {
   }
 
   // -inf for what a row does not see, from token `base` on.
-  __device__ __forceinline__ void mask(float4v (&s)[2][RT], float sign, int base, int g, const View<RT>& see) const {
+  __device__ __forceinline__ void mask(float4v (&s)[2][RT], int base, int g, const View<RT>& see) const {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       const uint32_t seen = seen_of(see.lim[rt], see.low(rt), base, g);
@@ -348,7 +355,7 @@ struct Rows {
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
           const uint32_t ones = all_ones_if(seen, t, r);
-          const float x = s[t][rt][r] * sign;
+          const float x = s[t][rt][r];
           s[t][rt][r] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & ones) | (0xFF800000u & ~ones));
         }
     }
@@ -435,19 +442,11 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// All bits of the bytes (of the FP16 values) of tokens that are seen: a word
-// for each tile t of a half page (for each pair of tokens).
+// All bits of the bytes of tokens that are seen, a word for each tile t of a
+// half page.
 __device__ __forceinline__ uint32_t keep_bytes(uint32_t seen, int t) {
   return ((((seen >> (16 * t)) & 15u) * 0x00204081u) & 0x01010101u) * 255u;
 }
-__device__ __forceinline__ u32x4 keep_halves(uint32_t seen) {
-  u32x4 k;
-#pragma unroll
-  for (int e = 0; e < 4; ++e)
-    k[e] = (all_ones_if(seen, e >> 1, 2 * (e & 1)) & 0xFFFFu) | (all_ones_if(seen, e >> 1, 2 * (e & 1) + 1) & 0xFFFF0000u);
-  return k;
-}
-
 // Values of a page that some rows see only a part of, codes of the D tiles of a
 // wavefront: what no row sees becomes zeros (what is there may be anything); NaN
 // that some rows see and others do not is taken out too, and put into the sums
@@ -511,16 +510,16 @@ struct Pages {
 };
 
 template <int RT>
-__device__ __forceinline__ View<RT> view_of(const AttentionArgs& a, int group, const Req& q, int lane, int first,
-                                            int rows) {
+__device__ __forceinline__ View<RT> view_of(const AttentionArgs& a, const AttnLaunch& l, const Req& q, int lane,
+                                            int first, int rows) {
   const int c16 = lane & 15, at = q.seq - q.rows + 1;
   View<RT> v;
   v.window = a.window;
 #pragma unroll
   for (int t = 0; t < RT; ++t)
-    v.lim[t] = t * 16 + c16 < rows ? at + (int)((uint32_t)(first + t * 16 + c16) / (uint32_t)group) : 0;
-  v.lim_min = uniform(at + (int)((uint32_t)first / (uint32_t)group));
-  v.lim_max = uniform(at + (int)((uint32_t)(first + rows - 1) / (uint32_t)group));
+    v.lim[t] = t * 16 + c16 < rows ? at + row_of(l, first + t * 16 + c16) : 0;
+  v.lim_min = uniform(at + row_of(l, first));
+  v.lim_max = uniform(at + row_of(l, first + rows - 1));
   v.low_min = a.window > 0 ? max(0, v.lim_min - a.window) : 0;
   v.low_max = a.window > 0 ? max(0, v.lim_max - a.window) : 0;
   return v;
@@ -530,13 +529,13 @@ __device__ __forceinline__ View<RT> view_of(const AttentionArgs& a, int group, c
 // dimensions 64 u + 16 g + 8 h + e, as the key units' 16 dimensions fall to the
 // lanes.  Rows behind `rows` are zeros.
 template <int DIM>
-__device__ __forceinline__ void load_query(const AttentionArgs& a, int group, const Req& r, int head, int lane,
-                                           int first, int rows, int t, half8 (&q)[DIM / 32]) {
+__device__ __forceinline__ void load_query(const AttentionArgs& a, const AttnLaunch& l, const Req& r, int head,
+                                           int lane, int first, int rows, int t, half8 (&q)[DIM / 32]) {
   const int c16 = lane & 15, g = lane >> 4;
   const bool in = t * 16 + c16 < rows;
-  const uint32_t rr = (uint32_t)(in ? first + t * 16 + c16 : 0), row = rr / (uint32_t)group;
-  const uint16_t* src = a.q + (int64_t)(r.row0 + (int)row) * a.q_stride +
-                        (int64_t)(head * group + (int)(rr - row * (uint32_t)group)) * DIM + 16 * g;
+  const int rr = in ? first + t * 16 + c16 : 0, row = row_of(l, rr);
+  const uint16_t* src = a.q + (int64_t)(r.row0 + row) * a.q_stride +
+                        (int64_t)(head * l.group + (rr - row * l.group)) * DIM + 16 * g;
 #pragma unroll
   for (int k = 0; k < DIM / 32; ++k)
     q[k] = in ? *reinterpret_cast<const half8*>(src + 64 * (k >> 1) + 8 * (k & 1)) : half8{};
@@ -560,22 +559,21 @@ struct Slot {
   __device__ static int row(int rt, int c16) { return kSums + (rt * 16 + c16) * 8; }
 };
 
-// Four dimensions of a row: y when the piece is the whole segment.
-__device__ __forceinline__ void write_y(const AttentionArgs& a, int group, const Req& q, int head, int rr, int dim0,
-                                        int dim, float4v sum, float weight) {
-  const int row = (int)((uint32_t)rr / (uint32_t)group);
+// Four dimensions of row `rr` of a segment: y.
+__device__ __forceinline__ void write_y(const AttentionArgs& a, const AttnLaunch& l, const Req& q, int head, int rr,
+                                        int dim0, int dim, float4v sum, float weight) {
+  const int row = row_of(l, rr);
   half4 h;
+  float inverse = 1.0f / weight;
   if (weight == 0.0f) {
     // nothing seen gives zeros; tokens seen but no weight (every score -inf) has no value
-    const int lim = q.seq - q.rows + row + 1;
-    const _Float16 x = lim > 0 ? (_Float16)__builtin_nanf("") : (_Float16)0;
-    h = half4{x, x, x, x};
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = (_Float16)(sum[e] / weight);
+    sum = float4v{0, 0, 0, 0};
+    inverse = q.seq - q.rows + row + 1 > 0 ? __builtin_nanf("") : 0.0f;
   }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) h[e] = (_Float16)(sum[e] * inverse);
   *reinterpret_cast<half4*>(a.y + (int64_t)(q.row0 + row) * a.y_stride +
-                            (int64_t)(head * group + rr - row * group) * dim + dim0) = h;
+                            (int64_t)(head * l.group + rr - row * l.group) * dim + dim0) = h;
 }
 
 // Arrivals.  True for the last of n workgroups that count themselves in at
@@ -595,45 +593,63 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, int n, uint32_t* 
   return last;
 }
 
-// Joins F fragments (f0 on, of one row tile) of `count` partial sums in order.
-// slot(i): the i-th one's slot.  All loads of kJoinChunk sums go out together.
-template <int DIM, int TILES, int F, typename SlotOf>
-__device__ __forceinline__ void join_fragments(__amdgpu_buffer_rsrc_t res, int lane, int f0, int count,
-                                               const SlotOf& slot, float4v (&sum)[F], float& top, float& weight) {
+// Joins the fragments of A row tiles (rt0 on) and B dimension tiles (d0 on) of
+// `count` partial sums in order.  slot(i): the i-th one's slot.  The loads of
+// CH sums go out together.
+template <int DIM, int TILES, int A, int B, typename SlotOf>
+__device__ __forceinline__ void join_fragments(__amdgpu_buffer_rsrc_t res, int lane, int rt0, int d0, int count,
+                                               const SlotOf& slot, float4v (&sum)[A][B], float (&top)[A],
+                                               float (&weight)[A]) {
   using S = Slot<DIM, TILES>;
-  constexpr int CH = F > 2 ? 4 : 8;
-  const int rt = f0 / S::DT, d0 = f0 % S::DT, c16 = lane & 15;
-  top = kLowest, weight = 0.0f;
+  constexpr int CH = A * B >= 3 ? 4 : 8;
+  const int c16 = lane & 15;
 #pragma unroll
-  for (int f = 0; f < F; ++f) sum[f] = float4v{0, 0, 0, 0};
+  for (int t = 0; t < A; ++t) {
+    top[t] = kLowest, weight[t] = 0.0f;
+#pragma unroll
+    for (int d = 0; d < B; ++d) sum[t][d] = float4v{0, 0, 0, 0};
+  }
 #pragma unroll 1
   for (int i0 = 0; i0 < count; i0 += CH) {
-    float4v o[CH][F];
-    float2v ml[CH];
-#pragma unroll
-    for (int i = 0; i < CH; ++i) {
-      const int at = slot(min(i0 + i, count - 1)) * S::kBytes;
-      ml[i] = __builtin_bit_cast(float2v, __builtin_amdgcn_raw_buffer_load_b64(res, S::row(rt, c16), at, kDevScope));
-#pragma unroll
-      for (int f = 0; f < F; ++f)
-        o[i][f] = __builtin_bit_cast(
-            float4v, __builtin_amdgcn_raw_buffer_load_b128(res, S::fragment(rt, d0 + f, lane), at, kDevScope));
-    }
-    float up = top;
-#pragma unroll
-    for (int i = 0; i < CH; ++i) up = fmaxf(up, ml[i][0]);
-    const float old = __builtin_amdgcn_exp2f(top - up);
-    top = up;
-    weight *= old;
-#pragma unroll
-    for (int f = 0; f < F; ++f) sum[f] *= old;
+    float4v o[CH][A][B];
+    float2v ml[CH][A];
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
       if (i0 + i < count) {
-        const float w = __builtin_amdgcn_exp2f(ml[i][0] - top);
-        weight += ml[i][1] * w;
+        const int at = slot(i0 + i) * S::kBytes;
 #pragma unroll
-        for (int f = 0; f < F; ++f) sum[f] += o[i][f] * w;
+        for (int t = 0; t < A; ++t) {
+          ml[i][t] = __builtin_bit_cast(float2v, __builtin_amdgcn_raw_buffer_load_b64(res, S::row(rt0 + t, c16), at, kDevScope));
+#pragma unroll
+          for (int d = 0; d < B; ++d)
+            o[i][t][d] = __builtin_bit_cast(
+                float4v, __builtin_amdgcn_raw_buffer_load_b128(res, S::fragment(rt0 + t, d0 + d, lane), at, kDevScope));
+        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < A; ++t) {
+          ml[i][t] = float2v{kLowest, 0.0f};
+#pragma unroll
+          for (int d = 0; d < B; ++d) o[i][t][d] = float4v{0, 0, 0, 0};
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < A; ++t) {
+      float up = top[t];
+#pragma unroll
+      for (int i = 0; i < CH; ++i) up = fmaxf(up, ml[i][t][0]);
+      const float old = __builtin_amdgcn_exp2f(top[t] - up);
+      top[t] = up;
+      weight[t] *= old;
+#pragma unroll
+      for (int d = 0; d < B; ++d) sum[t][d] *= old;
+#pragma unroll
+      for (int i = 0; i < CH; ++i) {
+        const float w = __builtin_amdgcn_exp2f(ml[i][t][0] - up);
+        weight[t] += ml[i][t][1] * w;
+#pragma unroll
+        for (int d = 0; d < B; ++d) sum[t][d] += o[i][t][d] * w;
       }
     }
   }
@@ -645,15 +661,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t partial_of(const AttnLaunch& l
 
 // After the pieces' sums are stored: the last workgroup of a segment (of a
 // group of its pieces first, when there are many) joins them in order and
-// writes y.  Each wavefront takes a share of the fragments.
+// writes y.  Each wavefront takes dimension tiles of its own, all rows.
 template <int DIM, int TILES, int WAVES>
 __device__ __forceinline__ void join_pieces(const AttentionArgs& a, const AttnLaunch& l, const Item& it, const Req& q,
                                             int lane, int wave, int row_first, int rows_here, uint32_t* s_arrival) {
   using S = Slot<DIM, TILES>;
-  constexpr int PER = TILES * S::DT / WAVES;  // fragments of a wavefront
-  constexpr int F = PER >= 4 ? 4 : PER >= 2 ? 2 : 1;
-  constexpr int SHARES = TILES * S::DT / F;
-  static_assert(S::DT % F == 0 && SHARES * F == TILES * S::DT, "a share lies in one row tile");
   const int c16 = lane & 15, g = lane >> 4;
   const __amdgpu_buffer_rsrc_t res = partial_of(l);
   uint32_t* const counters = (uint32_t*)a.scratch;
@@ -676,25 +688,22 @@ __device__ __forceinline__ void join_pieces(const AttentionArgs& a, const AttnLa
   for (;;) {
     auto slot = [&](int i) { return outer ? l.slots + (it.first + start_of(i)) / 2 : first + i; };
 #pragma unroll 1
-    for (int share = wave; share < SHARES; share += WAVES) {
-      const int f0 = share * F, rt = f0 / S::DT, d0 = f0 % S::DT;
-      if (rt * 16 >= rows_here) break;
-      float4v sum[F];
-      float top, weight;
-      join_fragments<DIM, TILES, F>(res, lane, f0, count, slot, sum, top, weight);
-      if (inner) {
-        const int at = (l.slots + first / 2) * S::kBytes;
+    for (int d = wave; d < S::DT; d += WAVES) {
+      float4v sum[TILES][1];
+      float top[TILES], weight[TILES];
+      join_fragments<DIM, TILES, TILES, 1>(res, lane, 0, d, count, slot, sum, top, weight);
+      const int at = (l.slots + first / 2) * S::kBytes;
 #pragma unroll
-        for (int f = 0; f < F; ++f)
-          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum[f]), res, S::fragment(rt, d0 + f, lane), at,
+      for (int rt = 0; rt < TILES; ++rt) {
+        if (inner) {
+          __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum[rt][0]), res, S::fragment(rt, d, lane), at,
                                                  kDevScope);
-        if (d0 == 0 && g == 0)
-          __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, float2v{top, weight}), res, S::row(rt, c16), at,
-                                                kDevScope);
-      } else if (rt * 16 + c16 < rows_here) {
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-          write_y(a, l.group, q, it.head, row_first + rt * 16 + c16, 16 * (d0 + f) + 4 * g, DIM, sum[f], weight);
+          if (d == 0 && g == 0)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, float2v{top[rt], weight[rt]}), res,
+                                                  S::row(rt, c16), at, kDevScope);
+        } else if (rt * 16 + c16 < rows_here) {
+          write_y(a, l, q, it.head, row_first + rt * 16 + c16, 16 * d + 4 * g, DIM, sum[rt][0], weight[rt]);
+        }
       }
     }
     if (!inner) return;
@@ -724,7 +733,7 @@ struct FewLds {
   half8 p[2][W][2][RT][64];  // operands of the second product: page, k-step, row tile, lane
   half8 q[KS][RT][64];       // operands of the first
   float m[2][ROWS][W];       // the pages' maxima
-  float last[W][ROWS], sum[W][ROWS];
+  float last[ROWS][W], sum[ROWS][W];
 };
 
 template <int DIM, int RT>
@@ -747,13 +756,17 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
     if (it.request < 0) break;  // past the last item: the whole workgroup leaves
     const int row_first = it.tile * ROWS;  // among the segment's rows
     const int rows_here = min(ROWS, q.rows * l.group - row_first);
-    const View<RT> see = view_of<RT>(a, l.group, q, lane, row_first, rows_here);
+    const View<RT> see = view_of<RT>(a, l, q, lane, row_first, rows_here);
     // the piece's pages that the tile sees
     const int lo = max(q.first_page + (int)((int64_t)q.pages * it.piece / it.pieces), see.low_min / kKvPage);
     const int hi = min(q.first_page + (int)((int64_t)q.pages * (it.piece + 1) / it.pieces),
                        (see.lim_max + kKvPage - 1) / kKvPage);
     const int count = max(0, hi - lo);
     const int32_t* const table = a.table + it.request * a.table_stride;
+    // (the queries first: loads return in order)
+    static_assert(RT <= W, "a row tile of queries per wavefront");
+    half8 qr[KS];
+    if (wave < RT) load_query<DIM>(a, l, q, it.head, lane, row_first, rows_here, wave, qr);
     Pages now;  // of the 64 pages around the present ones
     now.load(a, table, it.head, q.bad, lane, lo, 1, hi);
 
@@ -781,11 +794,9 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
 #pragma unroll
       for (int j = 0; j < W; ++j) load_values(now.template offset_at<DIM>(a, it.head, min(j, count - 1)), v[j]);
     }
-    for (int t = wave; t < RT; t += W) {
-      half8 qr[KS];
-      load_query<DIM>(a, l.group, q, it.head, lane, row_first, rows_here, t, qr);
+    if (wave < RT) {
 #pragma unroll
-      for (int i = 0; i < KS; ++i) s.q[i][t][lane] = qr[i];
+      for (int i = 0; i < KS; ++i) s.q[i][wave][lane] = qr[i];
     }
     lds_barrier();
 
@@ -830,14 +841,15 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
             }
           }
         load_keys(next.template offset_at<DIM>(a, it.head, next_at + min(wave, last)));
-        if (base + kKvPage > see.lim_min || base < see.low_max || !(kc > 0.0f)) {
-          // a negative factor moves to the scores; for 0 any does, with zeros;
-          // what a row does not see is -inf
-          float sign = 1.0f;
-          if (!(kc > 0.0f)) {
-            sign = kc == 0.0f ? 0.0f : -1.0f;
-            kc = kc == 0.0f ? 1.0f : -kc;
-          }
+        if (__builtin_expect(!(kc > 0.0f), 0)) {  // a negative factor moves to the scores; for 0 any does, with zeros
+          const float sign = kc == 0.0f ? 0.0f : -1.0f;
+          kc = kc == 0.0f ? 1.0f : -kc;
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) x[t][rt] *= sign;
+        }
+        if (base + kKvPage > see.lim_min || base < see.low_max) {  // what a row does not see is -inf
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
@@ -848,7 +860,7 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
                   const uint32_t ones = all_ones_if(seen, t, r);
-                  const float z = x[2 * half + t][rt][r] * sign;
+                  const float z = x[2 * half + t][rt][r];
                   x[2 * half + t][rt][r] =
                       __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, z) & ones) | (0xFF800000u & ~ones));
                 }
@@ -958,16 +970,19 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
     for (int rt = 0; rt < RT; ++rt) {
       sum[rt] += __shfl_xor(sum[rt], 16);
       sum[rt] += __shfl_xor(sum[rt], 32);
-      if (g == 0) s.last[wave][rt * 16 + c16] = m[rt], s.sum[wave][rt * 16 + c16] = sum[rt];
+      if (g == 0) s.last[rt * 16 + c16][wave] = m[rt], s.sum[rt * 16 + c16][wave] = sum[rt];
       sum[rt] = 0.0f;
     }
     lds_barrier();
-#pragma unroll 1
-    for (int w = 0; w < W; ++w) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        sum[rt] += s.sum[w][rt * 16 + c16] * __builtin_amdgcn_exp2f(s.last[w][rt * 16 + c16] - top[rt]);
-    }
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int w = 0; w < W; w += 4) {
+        const float4v mw = *reinterpret_cast<const float4v*>(&s.last[rt * 16 + c16][w]);
+        const float4v sw = *reinterpret_cast<const float4v*>(&s.sum[rt * 16 + c16][w]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[rt] += sw[e] * __builtin_amdgcn_exp2f(mw[e] - top[rt]);
+      }
     const __amdgpu_buffer_rsrc_t res = partial_of(l);
     const int slot = (it.first + it.piece) * S::kBytes;
 #pragma unroll
@@ -977,7 +992,7 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
       for (int d = 0; d < DW; ++d) {
         if (it.pieces == 1) {
           if (rt * 16 + c16 < rows_here)
-            write_y(a, l.group, q, it.head, row_first + rt * 16 + c16, 16 * (wave * DW + d) + 4 * g, DIM, o[d][rt], sum[rt]);
+            write_y(a, l, q, it.head, row_first + rt * 16 + c16, 16 * (wave * DW + d) + 4 * g, DIM, o[d][rt], sum[rt]);
         } else {
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, o[d][rt]), res,
                                                  S::fragment(rt, wave * DW + d, lane), slot, kDevScope);
@@ -1011,6 +1026,7 @@ __global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_
   extern __shared__ __attribute__((aligned(16))) half8 s_pages[];
   half8(*const s_k)[KF * 2 * 64] = reinterpret_cast<half8(*)[KF * 2 * 64]>(s_pages);
   half8(*const s_v)[VF * 2 * 64] = reinterpret_cast<half8(*)[VF * 2 * 64]>(s_pages + 2 * KF * 2 * 64);
+  __shared__ __attribute__((aligned(16))) int s_nan[2][kManyWaves];  // the page at a buffer's values hold NaN
   const int wave = uniform((int)threadIdx.x >> 6);
 
   for (int block = blockIdx.x;; block += gridDim.x) {
@@ -1025,9 +1041,8 @@ __global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_
     const int row_first = tile_first + wave * 16 * RT;       // this wavefront's
     const int rows_here = min(16 * RT, tile_rows - wave * 16 * RT);
     const bool some = rows_here > 0;
-    const View<1> all = view_of<1>(a, l.group, q, lane, tile_first, tile_rows);
-    View<RT> see = view_of<RT>(a, l.group, q, lane, row_first, some ? rows_here : 1);
-    if (!some) see.lim_min = 0;  // no page is an ordinary one
+    const View<1> all = view_of<1>(a, l, q, lane, tile_first, tile_rows);
+    const View<RT> see = view_of<RT>(a, l, q, lane, row_first, some ? rows_here : 1);
     const int lo = max(q.first_page + (int)((int64_t)q.pages * it.piece / it.pieces), all.low_min / kKvPage);
     const int hi = min(q.first_page + (int)((int64_t)q.pages * (it.piece + 1) / it.pieces),
                        (all.lim_max + kKvPage - 1) / kKvPage);
@@ -1036,7 +1051,7 @@ __global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_
     pages.load(a, table, it.head, q.bad, lane, lo, 1, hi);
     half8 qr[RT][KS];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) load_query<DIM>(a, l.group, q, it.head, lane, row_first, rows_here, rt, qr[rt]);
+    for (int rt = 0; rt < RT; ++rt) load_query<DIM>(a, l, q, it.head, lane, row_first, rows_here, rt, qr[rt]);
     R rows;
     rows.begin(Pages::at(pages.vs, 0));
 
@@ -1055,7 +1070,25 @@ __global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_
       for (int i = 0; i < PER; ++i)
         vr[i] = *reinterpret_cast<const u32x4*>(vs + ((wave * PER + i) * 16 + c16) * kKvPage + 16 * g);
     };
-    auto put = [&](int buffer) {
+    // Values of a page that some rows of the tile see only a part of: what none
+    // sees becomes zeros (what is there may be anything), and so does NaN, of
+    // which a flag is left.
+    auto put = [&](int buffer, int base) {
+      if (base + kKvPage > all.lim_min || base < all.low_max) {
+        uint32_t any = 0;
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          const uint32_t keep = keep_bytes(seen_of(all.lim_max, all.low_min, base + 32 * (t >> 1), g), t & 1);
+#pragma unroll
+          for (int i = 0; i < PER; ++i) {
+            const uint32_t x = vr[i][t] & keep, n = nan_bytes(x) >> 7;
+            any |= n;
+            vr[i][t] = x & ~(n * 255u);
+          }
+        }
+        const uint64_t some_nan = __ballot(any != 0);
+        if (lane == 0) s_nan[buffer][wave] = some_nan != 0;
+      }
 #pragma unroll
       for (int i = 0; i < PER; ++i) {
         half8 f[2];
@@ -1069,94 +1102,62 @@ __global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_
     };
     if (lo < hi) {
       load(pages.offset_at<DIM>(a, it.head, 0));
-      put(0);
+      put(0, lo * kKvPage);
     }
-    int page = lo;
-    float kc = 0.0f, vs = 0.0f;
-    int buffer = 0;
-    // Page `page` and the next one's way into the other buffer; every
-    // wavefront of the workgroup goes through the same barriers.
-    const auto key = [&](int u, int t, int h) { return s_k[buffer][((u * 4 + t) * 2 + h) * 64 + lane]; };
-    const auto query = [&](int i, int rt) { return qr[rt][i]; };
-    const auto open = [&] {
-      const int i = (page - lo) & 63;
-      buffer = (page - lo) & 1;
-      kc = Pages::at(pages.kc, i), vs = Pages::at(pages.vs, i);
-      __syncthreads();  // this page is in LDS, the other buffer has been read
+    for (int page = lo; page < hi; ++page) {
+      const int i = (page - lo) & 63, buffer = (page - lo) & 1, base = page * kKvPage;
+      float kc = Pages::at(pages.kc, i), vs = Pages::at(pages.vs, i);
+      const int64_t offset = pages.offset_at<DIM>(a, it.head, i);
+      lds_barrier();  // this page is in LDS, the other buffer has been read
       if (page + 1 < hi) {
         if (i == 63) pages.load(a, table, it.head, q.bad, lane, page + 1, 1, hi);
         load(pages.offset_at<DIM>(a, it.head, (i + 1) & 63));
       }
-    };
-    if (page < hi) open();
-    while (page < hi) {
-      // the loop over ordinary pages by itself, which keeps the sums in place
-      while (rows.ordinary(kc, vs, page * kKvPage, see)) {
+      if (some && base < see.lim_max && base + kKvPage > see.low_min) {
+        const bool masked = base + kKvPage > see.lim_min || base < see.low_max;
+        typename R::Edge e{1.0f, false};
+        if (__builtin_expect(!rows.ordinary(kc, vs), 0)) e = rows.settle(kc, vs);
         const float lift = __builtin_amdgcn_logf(vs / rows.vref), drop = rows.vref / vs;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           float4v s[2][RT];
           half8 p[RT];
-          rows.scores(key, query, half, s);
+          rows.scores([&](int u, int t, int h) { return s_k[buffer][((u * 4 + t) * 2 + h) * 64 + lane]; },
+                      [&](int i, int rt) { return qr[rt][i]; }, half, s);
+          if (__builtin_expect(e.sign != 1.0f, 0)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int rt = 0; rt < RT; ++rt) s[t][rt] *= e.sign;
+          }
+          if (masked) rows.mask(s, base + 32 * half, g, see);
           rows.weigh(s, kc, lift, drop, p);
+          if (__builtin_expect(e.nothing, 0)) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) p[rt] = half8{};
+          }
           rows.accumulate([&](int d) { return s_v[buffer][(d * 2 + half) * 64 + lane]; }, p);
         }
-        if (page + 1 < hi) put(buffer ^ 1);
-        if (++page == hi) break;
-        open();
-      }
-      if (page < hi) {
-        const int base = page * kKvPage;
-        if (some && base < see.lim_max && base + kKvPage > see.low_min) {
-          const typename R::Edge e = rows.settle(kc, vs);
-          const float lift = __builtin_amdgcn_logf(vs / rows.vref), drop = rows.vref / vs;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const int at = base + 32 * half;
-            // values that no row of the wavefront sees become zeros (what is
-            // there may be anything), and NaN that some see and others do not
-            u32x4 keep = keep_halves(seen_of(see.lim_max, see.low_min, at, g));
-            if (e.nothing) keep = u32x4{0, 0, 0, 0};
-            const auto value = [&](int d) {
-              return __builtin_bit_cast(half8, __builtin_bit_cast(u32x4, s_v[buffer][(d * 2 + half) * 64 + lane]) & keep);
-            };
-            bool any = false;
+        if (base + kKvPage > all.lim_min || base < all.low_max) {
+          const int4 nan = *reinterpret_cast<const int4*>(s_nan[buffer]);
+          if (__builtin_expect((nan.x | nan.y | nan.z | nan.w) != 0, 0)) {
+            // NaN that some rows see: from the page's codes
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-              const half8 x = value(d);
+              u32x4 x = *reinterpret_cast<const u32x4*>(a.cache.v + offset + (16 * d + c16) * kKvPage + 16 * g);
+              asm volatile("" : "+v"(x) : : "memory");  // one at a time: rare, and its registers are the loop's
 #pragma unroll
-              for (int i = 0; i < 8; ++i) any |= x[i] != x[i];
-            }
-            float4v s[2][RT];
-            half8 p[RT];
-            rows.scores(key, query, half, s);
-            rows.mask(s, e.sign, at, g, see);
-            rows.weigh(s, kc, lift, drop, p);
-            if (__builtin_expect(__ballot(any) != 0, 0)) {
+              for (int half = 0; half < 2; ++half) {
+                const half8 n = decode_e4m3x8((nan_bytes(x[2 * half]) >> 7) * 0x38u, (nan_bytes(x[2 * half + 1]) >> 7) * 0x38u);
 #pragma unroll
-              for (int d = 0; d < DT; ++d) {
-                half8 x = value(d);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] != x[i] ? (_Float16)1 : (_Float16)0;
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) spread_nan(x, seen_of(see.lim[rt], see.low(rt), at, g), rows.o[d][rt]);
+                for (int rt = 0; rt < RT; ++rt)
+                  spread_nan(n, seen_of(see.lim[rt], see.low(rt), base + 32 * half, g), rows.o[d][rt]);
               }
-              rows.accumulate(
-                  [&](int d) {
-                    half8 x = value(d);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[i] = x[i] != x[i] ? (_Float16)0 : x[i];
-                    return x;
-                  },
-                  p);
-            } else {
-              rows.accumulate(value, p);
             }
           }
         }
-        if (page + 1 < hi) put(buffer ^ 1);
-        if (++page < hi) open();
       }
+      if (page + 1 < hi) put(buffer ^ 1, base + kKvPage);
     }
 
     const __amdgpu_buffer_rsrc_t res = partial_of(l);
@@ -1171,7 +1172,7 @@ __global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_
         const float4v sum = rows.o[d][rt] * rows.vref;
         if (it.pieces == 1) {
           if (rt * 16 + c16 < rows_here)
-            write_y(a, l.group, q, it.head, row_first + rt * 16 + c16, 16 * d + 4 * g, DIM, sum, weight);
+            write_y(a, l, q, it.head, row_first + rt * 16 + c16, 16 * d + 4 * g, DIM, sum, weight);
         } else {
           __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, sum), res,
                                                  S::fragment(wave * RT + rt, d, lane), slot, 0);
@@ -1191,7 +1192,7 @@ __global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_
 template <int DIM, int TILES>
 __global__ __launch_bounds__(kManyWaves * 64) void attention_join_kernel(AttentionArgs a, AttnLaunch l) {
   using S = Slot<DIM, TILES>;
-  constexpr int F = 2, SHARES = TILES * S::DT / F;
+  constexpr int B = 2, SHARES = TILES * S::DT / B;  // a share: two dimension tiles of a row tile
   const int wave = uniform((int)threadIdx.x >> 6), lane = threadIdx.x & 63, c16 = lane & 15, g = lane >> 4;
   for (int block = blockIdx.x;; block += gridDim.x) {
     Req q;
@@ -1201,16 +1202,16 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention_join_kernel(Attenti
     const int row_first = it.tile * 16 * TILES;
     const int rows_here = min(16 * TILES, q.rows * l.group - row_first);
     for (int share = it.piece * kManyWaves + wave; share < SHARES; share += it.pieces * kManyWaves) {
-      const int f0 = share * F, rt = f0 / S::DT, d0 = f0 % S::DT;
+      const int rt = share * B / S::DT, d0 = share * B % S::DT;
       if (rt * 16 >= rows_here) break;
-      float4v sum[F];
-      float top, weight;
-      join_fragments<DIM, TILES, F>(partial_of(l), lane, f0, it.pieces, [&](int i) { return it.first + i; }, sum, top,
-                                    weight);
+      float4v sum[1][B];
+      float top[1], weight[1];
+      join_fragments<DIM, TILES, 1, B>(partial_of(l), lane, rt, d0, it.pieces, [&](int i) { return it.first + i; }, sum,
+                                       top, weight);
       if (rt * 16 + c16 < rows_here) {
 #pragma unroll
-        for (int f = 0; f < F; ++f)
-          write_y(a, l.group, q, it.head, row_first + rt * 16 + c16, 16 * (d0 + f) + 4 * g, DIM, sum[f], weight);
+        for (int d = 0; d < B; ++d)
+          write_y(a, l, q, it.head, row_first + rt * 16 + c16, 16 * (d0 + d) + 4 * g, DIM, sum[0][d], weight[0]);
       }
     }
   }
@@ -1260,14 +1261,12 @@ hipError_t launch_few(const AttentionArgs& a, const AttnLaunch& l, int64_t grid)
 
 template <int DIM>
 hipError_t launch_dim(const Form& f, const AttentionArgs& a, const AttnLaunch& l, int64_t grid) {
-  if (!f.many)
-    return f.tiles == 1   ? launch_few<DIM, 1>(a, l, grid)
-           : f.tiles == 2 ? launch_few<DIM, 2>(a, l, grid)
-                          : launch_few<DIM, 3>(a, l, grid);
-  if (f.tiles == 1) return launch_many<DIM, 1>(a, l, grid);
-  if constexpr (DIM < 256)
-    if (f.tiles == 3) return launch_many<DIM, 3>(a, l, grid);
-  return launch_many<DIM, 2>(a, l, grid);
+  if (f.tiles == 1) return f.many ? launch_many<DIM, 1>(a, l, grid) : launch_few<DIM, 1>(a, l, grid);
+  if constexpr (few_tiles(DIM) >= 3 && many_tiles(DIM) >= 3) {
+    if (f.tiles == 2) return f.many ? launch_many<DIM, 2>(a, l, grid) : launch_few<DIM, 2>(a, l, grid);
+    return f.many ? launch_many<DIM, 3>(a, l, grid) : launch_few<DIM, 3>(a, l, grid);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace
@@ -1287,6 +1286,7 @@ hipError_t launch_attention(const AttentionArgs& a) {
   AttnLaunch l;
   l.tile_rows = f.rows();
   l.group = group;
+  l.inverse = (uint32_t)(((uint64_t(1) << 32) + group - 1) / group);  // (not used for 1)
   l.target = wanted_pieces(f, segments);
   const size_t room = a.scratch_bytes > kKvZeroedBytes ? (a.scratch_bytes - kKvZeroedBytes) / slot_bytes(f, dim) : 0;
   l.slots = (int)((room > 3 * kMaxPieces ? 3 * kMaxPieces : room) * 2 / 3);
