@@ -47,7 +47,7 @@ constexpr float kLowest = -3e38f;     // the running maximum before any score
 
 // wavefronts of a workgroup, few rows: one per 16 dimensions up to eight
 constexpr int few_waves(int dim) { return dim == 64 ? 4 : 8; }
-constexpr int kManyWaves = 4;  // and many rows
+constexpr int kManyWaves = 8;  // and many rows
 constexpr int kMinPiecePages = 8;
 constexpr int kMaxPieces = 1024;   // pieces of a call with cut segments
 constexpr int kJoinDirect = 16;    // pieces joined in one step
@@ -57,7 +57,7 @@ static_assert((size_t)kMaxPieces * 2 * kCounterStep * 4 <= kKvZeroedBytes, "two 
 // The form and the 16-row tiles of a wavefront (of a workgroup, few rows) for
 // `rows` rows of a KV head (query rows x group).
 constexpr int few_tiles(int dim) { return dim == 256 ? 1 : 3; }   // what the registers hold
-constexpr int many_tiles(int dim) { return dim == 256 ? 1 : 3; }
+constexpr int many_tiles(int dim) { return dim == 256 ? 1 : 2; }
 struct Form {
   bool many;
   int tiles;
@@ -66,8 +66,7 @@ struct Form {
 inline Form form_for(int64_t rows, int dim) {
   const int64_t t = (rows + 15) / 16;
   if (t <= few_tiles(dim)) return {false, t < 1 ? 1 : (int)t};
-  const int each = (int)((t + kManyWaves - 1) / kManyWaves < 3 ? (t + kManyWaves - 1) / kManyWaves : 3);
-  return {true, each < many_tiles(dim) ? each : many_tiles(dim)};
+  return {true, t <= kManyWaves ? 1 : many_tiles(dim)};
 }
 
 struct AttnLaunch {
@@ -268,6 +267,36 @@ __device__ __forceinline__ uint32_t all_ones_if(uint32_t seen, int t, int r) {  
   return (uint32_t)__builtin_amdgcn_sbfe((int)seen, 16 * t + r, 1);
 }
 
+// -inf for what a row does not see of a page's scores.
+template <int RT>
+__device__ __forceinline__ void mask_page(float4v (&s)[4][RT], int base, int g, const View<RT>& see) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const uint32_t seen = seen_of(see.lim[rt], see.low(rt), base + 32 * half, g);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const uint32_t ones = all_ones_if(seen, t, r);
+          const float x = s[2 * half + t][rt][r];
+          s[2 * half + t][rt][r] =
+              __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & ones) | (0xFF800000u & ~ones));
+        }
+    }
+}
+
+// The largest of the lane's 16 scores of a row.  (Of products, which are never
+// signalling NaN: one instruction for two of them.)
+template <int RT>
+__device__ __forceinline__ float page_max(const float4v (&s)[4][RT], int rt) {
+  float mx = fmaxf(s[0][rt][0], s[0][rt][1]);
+#pragma unroll
+  for (int i = 2; i < 16; i += 2) mx = fmaxf(fmaxf(mx, s[i >> 2][rt][i & 3]), s[i >> 2][rt][(i & 3) + 1]);
+  return mx;
+}
+
 // The rows of a wavefront and their running sums.
 template <int DIM, int RT>
 struct Rows {
@@ -288,23 +317,9 @@ struct Rows {
     }
   }
 
-  // Whether a page's scales are positive and in proportion.  (Uniform.)
-  __device__ __forceinline__ bool ordinary(float kc, float vs) const {
-    return kc > 0.0f && vs <= vref * kScaleSlack && vs >= vref * kScaleLeast;
-  }
-
-  // What other scales need.
-  struct Edge {
-    float sign;     // of the scores
-    bool nothing;   // the values count for nothing
-  };
-  // Takes such scales to ordinary ones.
-  __device__ __forceinline__ Edge settle(float& kc, float& vs) {
-    Edge e{1.0f, false};
-    if (!(kc > 0.0f)) {  // a negative factor moves to the scores; for 0 any does, with zeros
-      e.sign = kc == 0.0f ? 0.0f : -1.0f;
-      kc = kc == 0.0f ? 1.0f : -kc;
-    }
+  // Takes a page's V scale to one that is positive and in proportion to vref
+  // (uniform); false when the values count for nothing beside the others.
+  __device__ __forceinline__ bool settle(float& vs) {
     if (vs > vref * kScaleSlack || (vs < vref * kScaleLeast && vs > vref * 0x1p-90f)) {
       const float f = vref / vs;
       vref = vs;
@@ -312,73 +327,44 @@ struct Rows {
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d][rt] *= f;
-    } else if (vs <= vref * kScaleLeast) {  // zero beside the others (a NaN goes on)
-      e.nothing = true;
+    } else if (vs <= vref * kScaleLeast) {  // (a NaN goes on)
       vs = vref;
+      return false;
     }
-    return e;
+    return true;
   }
 
-  // S^T of half a page.
-  //   key(u, t, h): operand h of the two of unit 4 u + g of token 16 t + c16;
-  //   query(k, rt): the B operand of k-step k (load_query).
-  template <typename Key, typename Query>
-  __device__ __forceinline__ void scores(const Key& key, const Query& query, int half, float4v (&s)[2][RT]) const {
+  // The operands of a product are read from LDS this many ahead of their use.
+  static constexpr int AHEAD = 2;
+  static constexpr int N = 4 * KS;  // operands of a page's keys; as many of its values
+
+  // S^T of a page.  key(i): operand i, of unit 4 (i / 8) + g, half i / 4 % 2, of
+  // token 16 (i % 4) + c16.  q[rt][k]: the B operand of k-step k (load_query).
+  template <typename Key>
+  static __device__ __forceinline__ void scores(const Key& key, const half8 (&q)[RT][KS], float4v (&s)[4][RT]) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) s[t][rt] = float4v{0, 0, 0, 0};
 #pragma unroll
-    for (int u = 0; u < DIM / 64; ++u) {
+    for (int i = 0; i < N; ++i) {
+      const half8 kf = key(i);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        half8 q[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) q[rt] = query(2 * u + h, rt);
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const half8 kf = key(u, 2 * half + t, h);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) s[t][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[rt], s[t][rt], 0, 0, 0);
-        }
-      }
+      for (int rt = 0; rt < RT; ++rt)
+        s[i & 3][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[rt][i >> 2], s[i & 3][rt], 0, 0, 0);
     }
   }
 
-  // -inf for what a row does not see, from token `base` on.
-  __device__ __forceinline__ void mask(float4v (&s)[2][RT], int base, int g, const View<RT>& see) const {
+  // Raises the maxima of rows that a page's scores (their largest a lane: high)
+  // pass by far.
+  __device__ __forceinline__ void raise(const float (&high)[RT]) {
+    bool far = false;
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      const uint32_t seen = seen_of(see.lim[rt], see.low(rt), base, g);
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const uint32_t ones = all_ones_if(seen, t, r);
-          const float x = s[t][rt][r];
-          s[t][rt][r] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, x) & ones) | (0xFF800000u & ~ones));
-        }
-    }
-  }
-
-  // The weights of half a page's scores, as the B operands of the second
-  // product, times vs / vref: exp2(kc score - m + lift), lift = log2(vs / vref);
-  // their FP32 sum times vref / vs (drop) goes to the sums.
-  __device__ __forceinline__ void weigh(float4v (&s)[2][RT], float kc, float lift, float drop, half8 (&p)[RT]) {
-    float top[RT];
-    bool raise = false;
-#pragma unroll
-    for (int rt = 0; rt < RT; ++rt) {
-      float mx = fmaxf(s[0][rt][0], s[0][rt][1]);
-#pragma unroll
-      for (int i = 2; i < 8; i += 2) mx = fmaxf(fmaxf(mx, s[i >> 2][rt][i & 3]), s[i >> 2][rt][(i & 3) + 1]);
-      top[rt] = mx * kc;
-      raise |= top[rt] > m[rt] + kMaxSlack;
-    }
-    if (__ballot(raise)) {
+    for (int rt = 0; rt < RT; ++rt) far |= high[rt] > m[rt] + kMaxSlack;
+    if (__ballot(far)) {
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        float mx = fmaxf(top[rt], __shfl_xor(top[rt], 16));
+        float mx = fmaxf(high[rt], __shfl_xor(high[rt], 16));
         mx = fmaxf(mx, __shfl_xor(mx, 32));
         const float up = fmaxf(m[rt], mx);
         const float f = __builtin_amdgcn_exp2f(m[rt] - up);
@@ -388,32 +374,72 @@ struct Rows {
         for (int d = 0; d < DT; ++d) o[d][rt] *= f;
       }
     }
+  }
+
+  // The weights of a page's scores s, as the B operands of the second product
+  // (p[h]: tokens of tiles 2 h and 2 h + 1), times vs / vref:
+  // exp2(score - m + lift), lift = log2(vs / vref), with their FP32 sum times
+  // vref / vs (drop) added to the sums; and the scores of the next page.  The
+  // two in turn, operand by operand, so that the vector and the matrix unit
+  // work at the same time: left to itself the compiler puts one behind the other.
+  template <typename Key>
+  __device__ __forceinline__ void weigh(float4v (&s)[4][RT], float lift, float drop, half8 (&p)[2][RT],
+                                        const Key& key, const half8 (&q)[RT][KS], float4v (&next)[4][RT]) {
+    half8 kf[AHEAD + 1];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) kf[i] = key(i);
+    float off[RT], part[RT][2];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const float off = lift - m[rt];
-      float part[2] = {0.0f, 0.0f};
+      off[rt] = lift - m[rt];
+      part[rt][0] = part[rt][1] = 0.0f;
+    }
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][rt][r], kc, off));
-          part[t] += w;
-          s[t][rt][r] = w;
-        }
-      sum[rt] = __builtin_fmaf(part[0] + part[1], drop, sum[rt]);
-      p[rt] = to_half8(s[0][rt], s[1][rt]);
+      for (int rt = 0; rt < RT; ++rt) next[t][rt] = float4v{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i + AHEAD < N) kf[(i + AHEAD) % (AHEAD + 1)] = key(i + AHEAD);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        next[i & 3][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[i % (AHEAD + 1)], q[rt][i >> 2], next[i & 3][rt], 0, 0, 0);
+#pragma unroll
+      for (int v = i * 16 * RT / N; v < (i + 1) * 16 * RT / N; ++v) {
+        const int rt = v / 16, t = v / 4 % 4, r = v % 4;
+        const float x = __builtin_amdgcn_exp2f(s[t][rt][r] + off[rt]);
+        part[rt][r & 1] += x;
+        s[t][rt][r] = x;
+        if (v % 8 == 7) p[t >> 1][rt] = to_half8(s[t - 1][rt], s[t][rt]);
+        if (v % 16 == 15) sum[rt] = __builtin_fmaf(part[rt][0] + part[rt][1], drop, sum[rt]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-  // O^T += V^T P^T over half a page.  value(d): the operand of dimension
-  // 16 d + c16, tokens 16 t + 4 g + r of the half's two tiles t.
+  // O^T += V^T P^T; and the next page's scores get their factor kc, and their
+  // largest is found.  value(i): the
+  // operand of dimension 16 (i / 2) + c16, tokens 16 t + 4 g + r of the tiles
+  // t = 2 (i % 2) and one more.
   template <typename Value>
-  __device__ __forceinline__ void accumulate(const Value& value, const half8 (&p)[RT]) {
+  __device__ __forceinline__ void accumulate(const Value& value, const half8 (&p)[2][RT], float4v (&next)[4][RT], float kc,
+                                             float (&high)[RT]) {
+    half8 vf[AHEAD + 1];
 #pragma unroll
-    for (int d = 0; d < DT; ++d) {
-      const half8 vf = value(d);
+    for (int i = 0; i < AHEAD; ++i) vf[i] = value(i);
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) o[d][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[rt], o[d][rt], 0, 0, 0);
+    for (int i = 0; i < N; ++i) {
+      if (i + AHEAD < N) vf[(i + AHEAD) % (AHEAD + 1)] = value(i + AHEAD);
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        o[i >> 1][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[i % (AHEAD + 1)], p[i & 1][rt], o[i >> 1][rt], 0, 0, 0);
+#pragma unroll
+      for (int v = i * 8 * RT / N; v < (i + 1) * 8 * RT / N; ++v) {  // a pair of scores at a time
+        const int rt = v / 8, t = v / 2 % 4, r = v % 2 * 2;
+        next[t][rt][r] *= kc, next[t][rt][r + 1] *= kc;
+        high[rt] = v % 8 ? fmaxf(fmaxf(high[rt], next[t][rt][r]), next[t][rt][r + 1]) : fmaxf(next[t][rt][r], next[t][rt][r + 1]);
+      }
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 };
@@ -818,7 +844,7 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
       const int next_at = left > 0 ? (at + W) & 63 : at, last = left > 0 ? min(W, left) - 1 : here - 1;
       if (wave < here) {
         // the weights of page i0 + wave
-        float kc = Pages::at(now.kc, at + wave);
+        const float kc = Pages::at(now.kc, at + wave);
         const int base = (lo + i0 + wave) * kKvPage;
         float4v x[4][RT];
 #pragma unroll
@@ -841,39 +867,18 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
             }
           }
         load_keys(next.template offset_at<DIM>(a, it.head, next_at + min(wave, last)));
-        if (__builtin_expect(!(kc > 0.0f), 0)) {  // a negative factor moves to the scores; for 0 any does, with zeros
-          const float sign = kc == 0.0f ? 0.0f : -1.0f;
-          kc = kc == 0.0f ? 1.0f : -kc;
 #pragma unroll
-          for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int rt = 0; rt < RT; ++rt) x[t][rt] *= sign;
-        }
+          for (int rt = 0; rt < RT; ++rt) x[t][rt] *= kc;
         if (base + kKvPage > see.lim_min || base < see.low_max) {  // what a row does not see is -inf
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const uint32_t seen = seen_of(see.lim[rt], see.low(rt), base + 32 * half, g);
-#pragma unroll
-              for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                  const uint32_t ones = all_ones_if(seen, t, r);
-                  const float z = x[2 * half + t][rt][r];
-                  x[2 * half + t][rt][r] =
-                      __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, z) & ones) | (0xFF800000u & ~ones));
-                }
-            }
+          mask_page<RT>(x, base, g, see);
         }
         float high[RT];
         bool raise = false;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          float mx = fmaxf(x[0][rt][0], x[0][rt][1]);
-#pragma unroll
-          for (int i = 2; i < 16; i += 2) mx = fmaxf(fmaxf(mx, x[i >> 2][rt][i & 3]), x[i >> 2][rt][(i & 3) + 1]);
-          high[rt] = mx * kc;
+          high[rt] = page_max<RT>(x, rt);
           raise |= high[rt] > m[rt] + kMaxSlack;
         }
         if (__ballot(raise)) {
@@ -893,7 +898,7 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
           for (int t = 0; t < 4; ++t)
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][rt][r], kc, -m[rt]));
+              const float w = __builtin_amdgcn_exp2f(x[t][rt][r] - m[rt]);
               part[t] += w;
               x[t][rt][r] = w;
             }
@@ -1012,21 +1017,48 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
 //
 // The workgroup converts a page to FP16 once, into the order of the products'
 // A operands (a conversion costs as much as two additions, and each wavefront
-// on its own would spend half its vector time on them).  Two buffers: while one
-// is used, the next page is on its way into registers, and it goes to the other
-// buffer behind the arithmetic, so there is one barrier a page.
+// on its own would spend half its vector time on them).  The scores of the next
+// page are computed beside the weights of this one, so that the matrix and the
+// vector units work at the same time; keys are therefore one page ahead of
+// values.  Two buffers of each, one barrier a page.  The codes come through a
+// ring of kRing pages in LDS (loads straight into it, each wavefront its own
+// part), so that a load has three pages' time to arrive; with the pages of
+// dimension 256 the ring does not fit, and they come through registers.
 // ---------------------------------------------------------------------------
+constexpr int kRing = 4;
+
+// A load of 16 bytes a lane into LDS: lane i's go to lds + 16 i.
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)lds)), "v"(offset), "s"(base)
+               : "memory", "m0");
+}
+
+// 16 bytes from LDS once no more than N of the loads above are on their way.
+template <int N>
+__device__ __forceinline__ u32x4 read_arrived(uint32_t lds) {
+  u32x4 x;
+  asm volatile("s_waitcnt vmcnt(%2)\n\tds_read_b128 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=&v"(x) : "v"(lds), "n"(N) : "memory");
+  return x;
+}
+
+template <int DIM>
+struct ManyLds {
+  half8 k[2][DIM / 8][64], v[2][DIM / 8][64];  // operands: buffer, operand, lane
+  int nan;                                     // values that only some rows of the tile see held NaN
+  static constexpr int RING = DIM < 256 ? kRing : 0;
+  static constexpr int LOADS = DIM / 8 / kManyWaves;  // 1 KiB of codes each, of a wavefront and page
+};
+
 template <int DIM, int RT>
-__global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_many_kernel(AttentionArgs a, AttnLaunch l) {
+__global__ __launch_bounds__(kManyWaves * 64) void attention_many_kernel(AttentionArgs a, AttnLaunch l) {
   using R = Rows<DIM, RT>;
   using S = Slot<DIM, RT * kManyWaves>;
   constexpr int DT = R::DT, KS = R::KS, ROWS = 16 * RT * kManyWaves;
-  constexpr int KF = DIM / 16, VF = DIM / 16;  // 16-byte-a-lane loads of a block of keys, of values
-  constexpr int PER = KF / kManyWaves;          // of a wavefront
-  extern __shared__ __attribute__((aligned(16))) half8 s_pages[];
-  half8(*const s_k)[KF * 2 * 64] = reinterpret_cast<half8(*)[KF * 2 * 64]>(s_pages);
-  half8(*const s_v)[VF * 2 * 64] = reinterpret_cast<half8(*)[VF * 2 * 64]>(s_pages + 2 * KF * 2 * 64);
-  __shared__ __attribute__((aligned(16))) int s_nan[2][kManyWaves];  // the page at a buffer's values hold NaN
+  using L = ManyLds<DIM>;
+  constexpr int LOADS = L::LOADS, RING = L::RING;
+  // the ring first, at LDS address 0 (there is no other LDS): 64 KiB, as a load's LDS address has 16 bits
+  extern __shared__ __attribute__((aligned(16))) uint8_t s_many[];
+  L& lds = *reinterpret_cast<L*>(s_many + RING * DIM * 128);
   const int wave = uniform((int)threadIdx.x >> 6);
 
   for (int block = blockIdx.x;; block += gridDim.x) {
@@ -1047,117 +1079,163 @@ __global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_
     const int hi = min(q.first_page + (int)((int64_t)q.pages * (it.piece + 1) / it.pieces),
                        (all.lim_max + kKvPage - 1) / kKvPage);
     const int32_t* const table = a.table + it.request * a.table_stride;
-    Pages pages;
-    pages.load(a, table, it.head, q.bad, lane, lo, 1, hi);
+    Pages now;  // of the 64 pages around the present ones
+    now.load(a, table, it.head, q.bad, lane, lo, 1, hi);
     half8 qr[RT][KS];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) load_query<DIM>(a, l, q, it.head, lane, row_first, rows_here, rt, qr[rt]);
+    if (threadIdx.x == 0) lds.nan = 0;
+    lds_barrier();
     R rows;
-    rows.begin(Pages::at(pages.vs, 0));
+    rows.begin(Pages::at(now.vs, 0));
 
-    // load n of the keys: unit 4 u + g of token 16 t + c16, n = 4 u + t; of the
-    // values: dimension 16 n + c16, group g
-    u32x4 kr[PER], vr[PER];
-    auto load = [&](int64_t offset) {
-      const uint8_t* const ks = a.cache.k + offset;
-      const uint8_t* const vs = a.cache.v + offset;
-#pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        const int n = wave * PER + i;
-        kr[i] = *reinterpret_cast<const u32x4*>(ks + (((n >> 2) * 4 + g) * kKvPage + (n & 3) * 16 + c16) * 16);
-      }
-#pragma unroll
-      for (int i = 0; i < PER; ++i)
-        vr[i] = *reinterpret_cast<const u32x4*>(vs + ((wave * PER + i) * 16 + c16) * kKvPage + 16 * g);
+    // The loads of a page, 1 KiB each, in turn to the wavefronts: keys, load n =
+    // 4 u + t: unit 4 u + g of token 16 t + c16; values, load n: dimension
+    // 16 n + c16, group g.  Keys are a page ahead of values.
+    const auto is_key = [&](int j) { return j * kManyWaves + wave < DIM / 16; };
+    const auto number = [&](int j) { return (j * kManyWaves + wave) % (DIM / 16); };
+    const auto place = [&](int j) {  // within the block
+      const int n = number(j);
+      return is_key(j) ? (((n >> 2) * 4 + g) * kKvPage + (n & 3) * 16 + c16) * 16 : (n * 16 + c16) * kKvPage + 16 * g;
     };
-    // Values of a page that some rows of the tile see only a part of: what none
-    // sees becomes zeros (what is there may be anything), and so does NaN, of
-    // which a flag is left.
-    auto put = [&](int buffer, int base) {
-      if (base + kKvPage > all.lim_min || base < all.low_max) {
+    const uint32_t ring = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)s_many + wave * (LOADS * 1024);
+    u32x4 held[LOADS];  // without a ring
+    const auto fetch = [&](int j, int64_t offset, int page) {
+      const uint8_t* const base = (is_key(j) ? a.cache.k : a.cache.v) + offset;
+      if constexpr (RING > 0)
+        load_to_lds(base, place(j), ring + (uint32_t)((page % RING) * (kManyWaves * LOADS) + j) * 1024u);
+      else
+        held[j] = *reinterpret_cast<const u32x4*>(base + place(j));
+    };
+    // Codes to operands.  Values of a page that some rows of the tile see only
+    // a part of: what none sees becomes zeros (what is there may be anything),
+    // and so does NaN, of which a flag is left.
+    const auto put = [&](int j, int page) {
+      u32x4 x;
+      if constexpr (RING > 0)
+        x = read_arrived<(RING - 1) * LOADS>(ring + (uint32_t)((page % RING) * (kManyWaves * LOADS) + j) * 1024u + lane * 16u);
+      else
+        x = held[j];
+      const int base = page * kKvPage;
+      const bool keys = is_key(j);
+      if (!keys && (base + kKvPage > all.lim_min || base < all.low_max)) {
         uint32_t any = 0;
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
-          const uint32_t keep = keep_bytes(seen_of(all.lim_max, all.low_min, base + 32 * (t >> 1), g), t & 1);
-#pragma unroll
-          for (int i = 0; i < PER; ++i) {
-            const uint32_t x = vr[i][t] & keep, n = nan_bytes(x) >> 7;
-            any |= n;
-            vr[i][t] = x & ~(n * 255u);
-          }
+          const uint32_t y = x[t] & keep_bytes(seen_of(all.lim_max, all.low_min, base + 32 * (t >> 1), g), t & 1);
+          const uint32_t n = nan_bytes(y) >> 7;
+          any |= n;
+          x[t] = y & ~(n * 255u);
         }
         const uint64_t some_nan = __ballot(any != 0);
-        if (lane == 0) s_nan[buffer][wave] = some_nan != 0;
+        if (lane == 0 && some_nan) lds.nan = 1;
       }
+      half8 f[2];
+      decode_fp8_fragment(x, f);
+      half8(*const to)[64] = keys ? lds.k[page & 1] : lds.v[page & 1];
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        half8 f[2];
-        decode_fp8_fragment(kr[i], f);
+      for (int h = 0; h < 2; ++h) to[number(j) * 2 + h][lane] = f[h];
+    };
+    // this wavefront's own pages among the workgroup's
+    const int my_lo = some ? max(lo, see.low_min / kKvPage) : hi;
+    const int my_hi = some ? min(hi, (see.lim_max + kKvPage - 1) / kKvPage) : hi;
+    float4v s[4][RT];  // the scores of page my_lo and on, one page ahead
+    float high[RT];    // and the largest of the lane's
+    Pages next = now;  // of the 64 pages behind those of `now`
+    // step `page`: the weights and values of `page`, the scores of page + 1; keys
+    // of page + 2 and values of page + 1 become operands; on their way: RING - 1
+    // pages more (without a ring: those two)
+    const auto offset_of = [&](int page, int at) {  // of `page` (the last one for any behind it), at most 64 behind lo + at
+      const int n = min(page, hi - 1) - lo;
+      const int id = (n >> 6) == (at >> 6) ? __builtin_amdgcn_readlane(now.id, n & 63) : __builtin_amdgcn_readlane(next.id, n & 63);
+      return ((int64_t)id * a.cache.heads + it.head) * (kKvPage * DIM);
+    };
+    int64_t values_at = 0;  // the offset of the page whose keys were fetched last
+    const auto fetch_all = [&](int page, int at, bool values) {  // keys of `page`, values of the one before
+      const int64_t keys_at = offset_of(page, at);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) s_k[buffer][((wave * PER + i) * 2 + h) * 64 + lane] = f[h];
-        decode_fp8_fragment(vr[i], f);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) s_v[buffer][((wave * PER + i) * 2 + h) * 64 + lane] = f[h];
-      }
+      for (int j = 0; j < LOADS; ++j) fetch(j, is_key(j) ? keys_at : values ? values_at : keys_at, is_key(j) ? page : values ? page - 1 : page);
+      values_at = keys_at;
     };
     if (lo < hi) {
-      load(pages.offset_at<DIM>(a, it.head, 0));
-      put(0, lo * kKvPage);
+      constexpr int FIRST = RING > 0 ? RING : 1;
+#pragma unroll
+      for (int i = 0; i < FIRST; ++i) fetch_all(lo + i, 0, i > 0);
+#pragma unroll
+      for (int j = 0; j < LOADS; ++j)
+        if (is_key(j)) put(j, lo);
     }
-    for (int page = lo; page < hi; ++page) {
-      const int i = (page - lo) & 63, buffer = (page - lo) & 1, base = page * kKvPage;
-      float kc = Pages::at(pages.kc, i), vs = Pages::at(pages.vs, i);
-      const int64_t offset = pages.offset_at<DIM>(a, it.head, i);
-      lds_barrier();  // this page is in LDS, the other buffer has been read
-      if (page + 1 < hi) {
-        if (i == 63) pages.load(a, table, it.head, q.bad, lane, page + 1, 1, hi);
-        load(pages.offset_at<DIM>(a, it.head, (i + 1) & 63));
+    for (int page = lo - 1; page < hi; ++page) {
+      const int at = max(page - lo, 0);
+      if (at > 0 && (at & 63) == 0) now = next;
+      if ((at & 63) == 32 && lo + (at | 63) + 1 < hi) next.load(a, table, it.head, q.bad, lane, lo + (at | 63) + 1, 1, hi);
+      lds_barrier();  // values of this page and keys of the next are in LDS, the other buffers have been read
+      if (lo < hi) {
+        constexpr int MORE = RING > 0 ? RING - 1 : 0;
+        fetch_all(page + 2 + MORE, at, true);
       }
-      if (some && base < see.lim_max && base + kKvPage > see.low_min) {
-        const bool masked = base + kKvPage > see.lim_min || base < see.low_max;
-        typename R::Edge e{1.0f, false};
-        if (__builtin_expect(!rows.ordinary(kc, vs), 0)) e = rows.settle(kc, vs);
-        const float lift = __builtin_amdgcn_logf(vs / rows.vref), drop = rows.vref / vs;
+      const auto key = [&](int i) { return lds.k[(page + 1) & 1][(i >> 3) * 8 + (i & 3) * 2 + (i >> 2 & 1)][lane]; };
+      const int behind = page + 1 - lo;  // the next page's place
+      const float next_kc = Pages::at((behind >> 6) == (at >> 6) ? now.kc : next.kc, behind & 63);
+      if (page >= my_lo && page < my_hi) {
+        float vs = Pages::at(now.vs, at & 63);
+        const int base = page * kKvPage;
+        bool counts = true;
+        if (__builtin_expect(!(vs <= rows.vref * kScaleSlack && vs >= rows.vref * kScaleLeast), 0)) counts = rows.settle(vs);
+        if (base + kKvPage > see.lim_min || base < see.low_max) {
+          mask_page<RT>(s, base, g, see);
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          float4v s[2][RT];
-          half8 p[RT];
-          rows.scores([&](int u, int t, int h) { return s_k[buffer][((u * 4 + t) * 2 + h) * 64 + lane]; },
-                      [&](int i, int rt) { return qr[rt][i]; }, half, s);
-          if (__builtin_expect(e.sign != 1.0f, 0)) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-              for (int rt = 0; rt < RT; ++rt) s[t][rt] *= e.sign;
-          }
-          if (masked) rows.mask(s, base + 32 * half, g, see);
-          rows.weigh(s, kc, lift, drop, p);
-          if (__builtin_expect(e.nothing, 0)) {
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) p[rt] = half8{};
-          }
-          rows.accumulate([&](int d) { return s_v[buffer][(d * 2 + half) * 64 + lane]; }, p);
+          for (int rt = 0; rt < RT; ++rt) high[rt] = page_max<RT>(s, rt);
         }
-        if (base + kKvPage > all.lim_min || base < all.low_max) {
-          const int4 nan = *reinterpret_cast<const int4*>(s_nan[buffer]);
-          if (__builtin_expect((nan.x | nan.y | nan.z | nan.w) != 0, 0)) {
-            // NaN that some rows see: from the page's codes
+        rows.raise(high);
+        const float drop = rows.vref * __builtin_amdgcn_rcpf(vs), lift = -__builtin_amdgcn_logf(drop);
+        half8 p[2][RT];
+        float4v ahead[4][RT];  // (of a page that is not there: of what the buffer holds, and not used)
+        rows.weigh(s, lift, drop, p, key, qr, ahead);
+        if (__builtin_expect(!counts, 0)) {
 #pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              u32x4 x = *reinterpret_cast<const u32x4*>(a.cache.v + offset + (16 * d + c16) * kKvPage + 16 * g);
-              asm volatile("" : "+v"(x) : : "memory");  // one at a time: rare, and its registers are the loop's
+          for (int h = 0; h < 2; ++h)
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const half8 n = decode_e4m3x8((nan_bytes(x[2 * half]) >> 7) * 0x38u, (nan_bytes(x[2 * half + 1]) >> 7) * 0x38u);
+            for (int rt = 0; rt < RT; ++rt) p[h][rt] = half8{};
+        }
+        rows.accumulate([&](int i) { return lds.v[page & 1][i][lane]; }, p, ahead, next_kc, high);
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt)
-                  spread_nan(n, seen_of(see.lim[rt], see.low(rt), base + 32 * half, g), rows.o[d][rt]);
-              }
-            }
-          }
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) s[t][rt] = ahead[t][rt];
+      } else if (page + 1 == my_lo && my_lo < my_hi) {
+        R::scores(key, qr, s);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+          for (int t = 0; t < 4; ++t) s[t][rt] *= next_kc;
+          high[rt] = page_max<RT>(s, rt);
         }
       }
-      if (page + 1 < hi) put(buffer ^ 1, base + kKvPage);
+      if (lo < hi) {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) put(j, is_key(j) ? page + 2 : page + 1);
+      }
+    }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // nothing more comes into LDS
+    lds_barrier();
+    if (__builtin_expect(uniform(lds.nan) != 0, 0)) {  // NaN into the rows that see it, from the pages' codes
+      for (int page = my_lo; page < my_hi; ++page) {
+        const int base = page * kKvPage, id = table[page];
+        if ((base + kKvPage <= all.lim_min && base >= all.low_max) || id < 0 || id >= a.cache.pages) continue;
+        const uint8_t* const values = a.cache.v + ((int64_t)id * a.cache.heads + it.head) * (kKvPage * DIM);
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+          const u32x4 x = *reinterpret_cast<const u32x4*>(values + (16 * d + c16) * kKvPage + 16 * g);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const half8 n = decode_e4m3x8((nan_bytes(x[2 * half]) >> 7) * 0x38u, (nan_bytes(x[2 * half + 1]) >> 7) * 0x38u);
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+              spread_nan(n, seen_of(see.lim[rt], see.low(rt), base + 32 * half, g), rows.o[d][rt]);
+          }
+        }
+      }
     }
 
     const __amdgpu_buffer_rsrc_t res = partial_of(l);
@@ -1182,7 +1260,7 @@ __global__ __launch_bounds__(kManyWaves * 64, DIM < 256 ? 2 : 1) void attention_
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u32x2, float2v{rows.m[rt], weight}), res,
                                               S::row(wave * RT + rt, c16), slot, 0);
     }
-    __syncthreads();  // LDS is free for the next item
+    lds_barrier();  // LDS is free for the next item
   }
 }
 
@@ -1225,13 +1303,9 @@ int64_t most_segments(int requests, int max_rows, int q_heads, int heads, int di
   return (int64_t)requests * heads * (tiles < 1 ? 1 : tiles);
 }
 
-// Pieces wanted: what the chip holds at once (one workgroup a CU of few rows, two
-// of many), or four times as many and smaller when there are so many segments
+// Pieces wanted: what the chip holds at once (a workgroup a CU), or four times as many and smaller when there are so many segments
 // that whole ones would leave it unevenly loaded.
-int wanted_pieces(const Form& f, int64_t segments) {
-  const int at_once = f.many ? 512 : 256;
-  return segments * 2 <= at_once ? at_once : kMaxPieces;
-}
+int wanted_pieces(int64_t segments) { return segments <= 128 ? 256 : kMaxPieces; }
 
 size_t slot_bytes(const Form& f, int dim) { return (size_t)f.rows() * dim * 4 + (size_t)f.rows() * 8; }
 
@@ -1248,8 +1322,8 @@ hipError_t launch_kernel(Kernel kernel, int threads, size_t lds, const Attention
 
 template <int DIM, int RT>
 hipError_t launch_many(const AttentionArgs& a, const AttnLaunch& l, int64_t grid) {
-  const hipError_t e = launch_kernel(attention_many_kernel<DIM, RT>, kManyWaves * 64, (size_t)4 * DIM / 16 * 2 * 1024, a,
-                                     l, grid);
+  const hipError_t e = launch_kernel(attention_many_kernel<DIM, RT>, kManyWaves * 64,
+                                     sizeof(ManyLds<DIM>) + (size_t)ManyLds<DIM>::RING * DIM * 128, a, l, grid);
   if (e != hipSuccess || l.slots == 0) return e;
   return launch_kernel(attention_join_kernel<DIM, RT * kManyWaves>, kManyWaves * 64, 0, a, l, grid);
 }
@@ -1262,9 +1336,9 @@ hipError_t launch_few(const AttentionArgs& a, const AttnLaunch& l, int64_t grid)
 template <int DIM>
 hipError_t launch_dim(const Form& f, const AttentionArgs& a, const AttnLaunch& l, int64_t grid) {
   if (f.tiles == 1) return f.many ? launch_many<DIM, 1>(a, l, grid) : launch_few<DIM, 1>(a, l, grid);
-  if constexpr (few_tiles(DIM) >= 3 && many_tiles(DIM) >= 3) {
+  if constexpr (DIM < 256) {
     if (f.tiles == 2) return f.many ? launch_many<DIM, 2>(a, l, grid) : launch_few<DIM, 2>(a, l, grid);
-    return f.many ? launch_many<DIM, 3>(a, l, grid) : launch_few<DIM, 3>(a, l, grid);
+    return launch_few<DIM, 3>(a, l, grid);
   }
   return hipErrorInvalidValue;
 }
@@ -1275,7 +1349,7 @@ size_t attention_scratch_bytes(int requests, int max_rows, int q_heads, int head
   const int64_t segments = most_segments(requests, max_rows, q_heads, heads, dim);
   if (table_width <= kMinPiecePages || segments >= kMaxPieces) return kKvZeroedBytes;
   const Form f = form_for((int64_t)max_rows * (q_heads / heads), dim);
-  const size_t slots = wanted_pieces(f, segments);
+  const size_t slots = wanted_pieces(segments);
   return kKvZeroedBytes + (slots + slots / 2) * slot_bytes(f, dim);
 }
 
@@ -1287,7 +1361,7 @@ hipError_t launch_attention(const AttentionArgs& a) {
   l.tile_rows = f.rows();
   l.group = group;
   l.inverse = (uint32_t)(((uint64_t(1) << 32) + group - 1) / group);  // (not used for 1)
-  l.target = wanted_pieces(f, segments);
+  l.target = wanted_pieces(segments);
   const size_t room = a.scratch_bytes > kKvZeroedBytes ? (a.scratch_bytes - kKvZeroedBytes) / slot_bytes(f, dim) : 0;
   l.slots = (int)((room > 3 * kMaxPieces ? 3 * kMaxPieces : room) * 2 / 3);
   if (l.slots < l.target) l.target = l.slots;
