@@ -38,7 +38,7 @@ constexpr int kArrivalStep = 4;                            // 32-bit words betwe
 static_assert((size_t)kKvMaxRequests * kArrivalStep * 4 <= kKvZeroedBytes, "a counter per request");
 constexpr int kVerifySpan = 64;       // chunks of a workgroup of the first kernel, at most
 constexpr int kVerifyRowsHeld = 16;   // rows of a request whose chunks' masses are held in LDS
-constexpr int kVerifyWgs = 2048;      // workgroups of the first kernel aimed at: eight a CU
+constexpr int kVerifyWgs = 1536;      // workgroups of the first kernel aimed at: the six a CU that its registers let reside
 
 // Chunks of a row: rows may start anywhere in a 16-byte granule, so a row's
 // tokens are counted from the granule's start (up to 7 places before it).
@@ -86,9 +86,7 @@ __device__ __forceinline__ double exp2_scaled(double d, const VerifyLaunch& l) {
   p = fma(p, r, 0.2402265069581299);
   p = fma(p, r, 0.6931471805459335);
   p = fma(p, r, 1.0);
-  const uint64_t bits = (uint64_t)__double_as_longlong(p);
-  const uint32_t high = (uint32_t)(bits >> 32) + ((uint32_t)__double_as_longlong(t) << 20);
-  return __longlong_as_double((long long)(((uint64_t)high << 32) | (uint32_t)bits));
+  return ldexp(p, (int)(uint32_t)(uint64_t)__double_as_longlong(t));
 }
 
 // The same, 0 from the lowest on.
