@@ -144,11 +144,13 @@ __global__ __launch_bounds__(kPlanThreads) void plan_round_kernel(PlanRoundArgs 
 //
 // The grid has two kinds of workgroups.  Query workgroups: a wavefront takes
 // one row and steps through its heads, HPW = 64 / LPH at a time, with the
-// row's cosines and sines in registers.  Cache workgroups: one (page, KV
-// head) each, found from the slots: the workgroup of row t goes on when t is
-// the first row of its page in the call, and gathers the rows of that page.
-// A page's scale is then one workgroup's business, whatever order the slots
-// come in: no atomics, no second launch.
+// row's cosines and sines in registers.  Cache workgroups: a few rows (one in
+// small calls) and one KV head; a workgroup does the pages that one of its rows
+// is the first of in the call, and gathers the other rows of such a page.  A
+// page's scale is then one workgroup's business, whatever order the slots come
+// in: no atomics, no second launch.  Small calls are bound by the chain of
+// dependent loads, so what a page most likely needs (the rows that follow its
+// first one, the old codes) is fetched before it is known to be needed.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWaves = kAppendThreads / kLanes;
@@ -310,20 +312,24 @@ __device__ __forceinline__ void append_queries(const RopeAppendArgs& a, int wg, 
   const int64_t wave = (int64_t)wg * kAppendWaves + (threadIdx.x >> 6);
   const int64_t row = wave / waves_per_row;
   if (row >= a.rows) return;  // a whole wavefront; no barrier follows
-  Rotor<float, DIM> rotor;
-  if (a.rot) rotor.angles(a, lane_at, (double)a.positions[row]);
   const int h0 = (int)(wave % waves_per_row) * steps * HPW + lane / LPH;
+  const uint16_t* const from = a.qkv + row * a.qkv_stride + lane_at * 8;
+  uint16_t* const to = a.q_out + row * a.q_stride + lane_at * 8;
+  half8 x = {}, next = {};
+  if (h0 < a.q_heads) x = load_half8(from + (int64_t)h0 * DIM);
+  Rotor<float, DIM> rotor;
+  rotor.turned = false;
+  if (a.rot) rotor.angles(a, lane_at, (double)a.positions[row]);
   for (int i = 0; i < steps; ++i) {
     const int h = h0 + i * HPW;
-    const bool in = h < a.q_heads;
-    half8 x = {};
-    if (in) x = load_half8(a.qkv + row * a.qkv_stride + (int64_t)h * DIM + lane_at * 8);
+    if (i + 1 < steps && h + HPW < a.q_heads) next = load_half8(from + (int64_t)(h + HPW) * DIM);
     float out[8];
     rotor.turn(a, lane_at, x, a.q_weight, out);
     half8 y;
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = (_Float16)out[e];
-    if (in) *reinterpret_cast<half8*>(a.q_out + row * a.q_stride + (int64_t)h * DIM + lane_at * 8) = y;
+    if (h < a.q_heads) *reinterpret_cast<half8*>(to + (int64_t)h * DIM) = y;
+    x = next;
   }
 }
 
@@ -341,10 +347,11 @@ __device__ __forceinline__ u32x4 recode16(u32x4 c, double ratio) {
 }
 
 template <int DIM>
-__device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, int head) {
+__device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, int32_t slot0, int head) {
   constexpr int LPH = DIM / 8;
   constexpr int RPS = kAppendThreads / LPH;  // rows a step of the workgroup takes
   constexpr int STEPS = kKvPage / RPS;
+  constexpr int UNITS = DIM * 4 / kAppendThreads;  // 16-byte units of the values' block, of a thread
   __shared__ int32_t s_row[kKvPage];      // the row at each offset of the page, -1: none
   __shared__ int32_t s_list[kKvPage];     // the offsets that are written, in order
   __shared__ int32_t s_earlier, s_count;
@@ -352,22 +359,30 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   __shared__ __attribute__((aligned(16))) uint8_t s_v[DIM * kKvPage];
   const int tid = threadIdx.x, lane = tid & 63, lane_at = tid % LPH;
 
-  const int32_t slot0 = a.slots[row0];
-  if (slot0 < 0 || slot0 >= a.cache.pages * kKvPage) return;
   const int32_t page = slot0 / kKvPage;
-  auto same_page = [&](int t) {
-    const int32_t s = a.slots[t];
-    return s >= 0 && s / kKvPage == page;
-  };
-  if (row0 > 0 && same_page(row0 - 1)) return;  // not the first of a run of rows
+  const int64_t block = (int64_t)page * a.cache.heads + head;
+  uint8_t* const kb = a.cache.k + block * (kKvPage * DIM);
+  uint8_t* const vb = a.cache.v + block * (kKvPage * DIM);
+
+  // the rows that follow, the scales and the old values: on their way
+  const uint16_t* const k_from = a.qkv + (int64_t)(a.q_heads + head) * DIM + lane_at * 8;
+  const uint16_t* const v_from = k_from + (int64_t)a.cache.heads * DIM;
+  const int near = min(row0 + tid / LPH, a.rows - 1);
+  half8 k_near = load_half8(k_from + near * a.qkv_stride), v_near = load_half8(v_from + near * a.qkv_stride);
+  int32_t pos_near = a.positions[near];
+  const float scale_k = a.cache.k_scale[block], scale_v = a.cache.v_scale[block];
+  u32x4 old[UNITS];
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i) old[i] = *reinterpret_cast<const u32x4*>(vb + (tid + i * kAppendThreads) * 16);
 
   if (tid < kKvPage) s_row[tid] = -1;
   if (tid == 0) s_earlier = 0;
   __syncthreads();
   for (int t = tid; t < a.rows; t += kAppendThreads) {
-    if (same_page(t)) {
+    const int32_t s = a.slots[t];
+    if (s >= 0 && s / kKvPage == page) {
       if (t < row0) s_earlier = 1;
-      atomicMax(&s_row[a.slots[t] % kKvPage], t);
+      atomicMax(&s_row[s % kKvPage], t);
     }
   }
   __syncthreads();
@@ -380,44 +395,36 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   __syncthreads();
   const int count = s_count;
   const bool fresh = s_row[0] >= 0;
-  const int64_t block = (int64_t)page * a.cache.heads + head;
-  uint8_t* const kb = a.cache.k + block * (kKvPage * DIM);
-  uint8_t* const vb = a.cache.v + block * (kKvPage * DIM);
-  const double old_k = fresh ? 0.0 : (double)a.cache.k_scale[block];
-  const double old_v = fresh ? 0.0 : (double)a.cache.v_scale[block];
+  const double old_k = fresh ? 0.0 : (double)scale_k, old_v = fresh ? 0.0 : (double)scale_v;
 
-  // the keys of one step: eight elements of row s_list[i]
-  auto key_of = [&](int i, double out[8]) {
-    const int t = s_row[s_list[i < count ? i : 0]];
-    Rotor<double, DIM> rotor;
-    if (a.rot) rotor.angles(a, lane_at, (double)a.positions[t]);
-    rotor.turn(a, lane_at, load_half8(a.qkv + t * a.qkv_stride + (int64_t)(a.q_heads + head) * DIM + lane_at * 8),
-               a.k_weight, out);
-  };
-  auto value_of = [&](int i) {
-    const int t = s_row[s_list[i < count ? i : 0]];
-    return load_half8(a.qkv + t * a.qkv_stride + (int64_t)(a.q_heads + a.cache.heads + head) * DIM +
-                      lane_at * 8);
-  };
-
-  // amax over the finite new values; the first step's keys stay in registers
-  // (a verify block or less), later ones are computed again below
-  double first[8], kmax = 0.0, vmax = 0.0;
-  half8 first_v;
-#pragma unroll 1
-  for (int st = 0; st < STEPS && st * RPS < count; ++st) {
-    const int i = st * RPS + tid / LPH;
-    double key[8];
-    key_of(i, key);
-    const half8 val = value_of(i);
+  // the keys, normed and rotated, and the raw values of the thread's rows (the
+  // rows i = RPS st + tid / LPH of the list), and their largest
+  double key[STEPS][8], kmax = 0.0, vmax = 0.0;
+  half8 val[STEPS];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const double k = fabs(key[e]), v = fabs((double)val[e]);
-      if (k < __builtin_inf()) kmax = fmax(kmax, k);
-      if (v < __builtin_inf()) vmax = fmax(vmax, v);
-      if (st == 0) first[e] = key[e];
+  for (int st = 0; st < STEPS; ++st) {
+    if (st * RPS < count) {
+      const int i = st * RPS + tid / LPH;
+      const int t = s_row[s_list[i < count ? i : 0]];
+      half8 x = k_near;
+      int32_t position = pos_near;
+      val[st] = v_near;
+      if (st > 0 || t != near) {
+        x = load_half8(k_from + t * a.qkv_stride);
+        val[st] = load_half8(v_from + t * a.qkv_stride);
+        position = a.positions[t];
+      }
+      Rotor<double, DIM> rotor;
+      rotor.turned = false;
+      if (a.rot) rotor.angles(a, lane_at, (double)position);
+      rotor.turn(a, lane_at, x, a.k_weight, key[st]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const double k = fabs(key[st][e]), v = fabs((double)val[st][e]);
+        if (k < __builtin_inf()) kmax = fmax(kmax, k);
+        if (v < __builtin_inf()) vmax = fmax(vmax, v);
+      }
     }
-    if (st == 0) first_v = val;
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
@@ -445,26 +452,16 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
       *p = recode16(*p, ratio);
     }
   }
-#pragma unroll 1
-  for (int st = 0; st < STEPS && st * RPS < count; ++st) {
-    const int i = st * RPS + tid / LPH;
-    double key[8];
-    half8 val;
-    if (st == 0) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) key[e] = first[e];
-      val = first_v;
-    } else {
-      key_of(i, key);
-      val = value_of(i);
-    }
+  for (int st = 0; st < STEPS; ++st) {
+    const int i = st * RPS + tid / LPH;
     if (i < count) {
       const int off = s_list[i], place = ((off >> 2) & 3) * 16 + (off >> 4) * 4 + (off & 3);
       uint32_t w[2] = {0, 0};
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        w[e >> 2] |= e4m3_code(key[e] * inv_k) << (8 * (e & 3));
-        s_v[(lane_at * 8 + e) * kKvPage + place] = (uint8_t)e4m3_code((double)val[e] * inv_v);
+        w[e >> 2] |= e4m3_code(key[st][e] * inv_k) << (8 * (e & 3));
+        s_v[(lane_at * 8 + e) * kKvPage + place] = (uint8_t)e4m3_code((double)val[st][e] * inv_v);
       }
       uint2 pair;
       pair.x = w[0], pair.y = w[1];
@@ -475,16 +472,16 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
 
   // values: 16-byte segments (dimension d, group g) of the tokens 16 t + 4 g + r
   const double ratio_v = grow_v ? old_v / new_v : 1.0;
-  for (int u = tid; u < DIM * 4; u += kAppendThreads) {
-    const int g = u & 3;
+#pragma unroll
+  for (int i = 0; i < UNITS; ++i) {
+    const int u = tid + i * kAppendThreads, g = u & 3;
     uint32_t fresh_bytes = 0;  // bit 4 t + r: token 16 t + 4 g + r is new
 #pragma unroll
     for (int j = 0; j < 16; ++j) fresh_bytes |= (uint32_t)(s_row[(j >> 2) * 16 + g * 4 + (j & 3)] >= 0) << j;
     if (!fresh_bytes && !grow_v) continue;
-    uint8_t* const p = vb + u * 16;
     u32x4 c = *reinterpret_cast<const u32x4*>(s_v + u * 16);
     if (fresh_bytes != 0xFFFFu) {
-      u32x4 o = *reinterpret_cast<const u32x4*>(p);
+      u32x4 o = old[i];
       if (grow_v) o = recode16(o, ratio_v);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
@@ -494,7 +491,7 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
         c[t] = (c[t] & mask) | (o[t] & ~mask);
       }
     }
-    *reinterpret_cast<u32x4*>(p) = c;
+    *reinterpret_cast<u32x4*>(vb + u * 16) = c;
   }
   if (tid == 0) {
     a.cache.k_scale[block] = (float)new_k;
@@ -502,11 +499,25 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   }
 }
 
+// The pages that rows row0 .. row0 + rows - 1 begin runs of (rows that follow one
+// another on one page).
 template <int DIM>
-__global__ __launch_bounds__(kAppendThreads) void rope_append_kernel(RopeAppendArgs a, int cache_wgs,
+__device__ __forceinline__ void append_rows(const RopeAppendArgs& a, int row0, int rows, int head) {
+  const int64_t places = a.cache.pages * kKvPage;
+  for (int t = row0; t < min(row0 + rows, a.rows); ++t) {  // (the whole workgroup agrees)
+    const int32_t slot = a.slots[t], before = t > 0 ? a.slots[t - 1] : -1;
+    if (slot < 0 || slot >= places) continue;
+    if (before >= 0 && before / kKvPage == slot / kKvPage) continue;
+    append_page<DIM>(a, t, slot, head);
+    if (rows > 1) __syncthreads();  // its LDS has been read
+  }
+}
+
+template <int DIM>
+__global__ __launch_bounds__(kAppendThreads) void rope_append_kernel(RopeAppendArgs a, int cache_wgs, int rows_per_wg,
                                                                      int waves_per_row, int steps) {
   if ((int)blockIdx.x < cache_wgs)
-    append_page<DIM>(a, (int)blockIdx.x / a.cache.heads, (int)blockIdx.x % a.cache.heads);
+    append_rows<DIM>(a, (int)blockIdx.x / a.cache.heads * rows_per_wg, rows_per_wg, (int)blockIdx.x % a.cache.heads);
   else
     append_queries<DIM>(a, (int)blockIdx.x - cache_wgs, waves_per_row, steps);
 }
@@ -520,10 +531,13 @@ hipError_t launch_append(const RopeAppendArgs& a) {
   int64_t steps = (int64_t)a.rows * groups / 2048;
   steps = steps < 1 ? 1 : steps > groups ? groups : steps;
   const int waves_per_row = (int)((groups + steps - 1) / steps);
-  const int64_t cache_wgs = (int64_t)a.rows * a.cache.heads;
+  // rows of a cache workgroup: one while those of all rows are on the chip at
+  // once, else so many that most workgroups have a page to do
+  const int rows_per_wg = (int64_t)a.rows * a.cache.heads <= 2048 ? 1 : 16;
+  const int64_t cache_wgs = (int64_t)((a.rows + rows_per_wg - 1) / rows_per_wg) * a.cache.heads;
   const int64_t query_wgs = ((int64_t)a.rows * waves_per_row + kAppendWaves - 1) / kAppendWaves;
   rope_append_kernel<DIM><<<dim3((uint32_t)(cache_wgs + query_wgs)), dim3(kAppendThreads), 0,
-                            (hipStream_t)a.stream>>>(a, (int)cache_wgs, waves_per_row, (int)steps);
+                            (hipStream_t)a.stream>>>(a, (int)cache_wgs, rows_per_wg, waves_per_row, (int)steps);
   return hipGetLastError();
 }
 
