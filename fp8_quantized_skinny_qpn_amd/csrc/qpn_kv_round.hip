@@ -207,6 +207,54 @@ __device__ __forceinline__ uint32_t e4m3_code(double x) {
   return sign | (uint32_t)((e + 7) * 8 + (int)rint(a * inv_step) - 8);
 }
 
+// Eight values times inv as E4M3 codes (byte e: element e).  The gfx950
+// conversion rounds FP32 correctly; what FP32 holds exactly goes through it.
+__device__ __forceinline__ float clamp448(float x) {  // (a NaN stays)
+  return x > 448.0f ? 448.0f : x < -448.0f ? -448.0f : x;
+}
+__device__ __forceinline__ uint2 pack_codes(const float f[8]) {
+  int lo = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(f[0]), clamp448(f[1]), 0, false);
+  lo = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(f[2]), clamp448(f[3]), lo, true);
+  int hi = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(f[4]), clamp448(f[5]), 0, false);
+  hi = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(f[6]), clamp448(f[7]), hi, true);
+  return make_uint2((uint32_t)lo, (uint32_t)hi);
+}
+// FP16 values: a product with a power of two is exact, another scale goes
+// through 64 bits.
+__device__ __forceinline__ uint2 value_codes(const half8& x, double inv, bool power_of_two) {
+  if (power_of_two) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[e] = (float)x[e] * (float)inv;
+    return pack_codes(f);
+  }
+  uint32_t w[2] = {0, 0};
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e >> 2] |= e4m3_code((double)x[e] * inv) << (8 * (e & 3));
+  return make_uint2(w[0], w[1]);
+}
+// Keys: their FP32 rounding goes the same way unless it lies on a border
+// between two codes (or among the subnormal ones, whose borders lie closer).
+__device__ __forceinline__ uint2 key_codes(const double x[8], double inv) {
+  float f[8];
+  bool near = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    f[e] = (float)(x[e] * inv);
+    near |= (__builtin_bit_cast(uint32_t, f[e]) & 0xFFFFFu) == 0x80000u || fabsf(f[e]) < 0x1p-6f;
+  }
+  uint2 w = pack_codes(f);
+  if (near) {
+    w = make_uint2(0, 0);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t c = e4m3_code(x[e] * inv) << (8 * (e & 3));
+      if (e < 4) w.x |= c; else w.y |= c;
+    }
+  }
+  return w;
+}
+
 __device__ __forceinline__ double e4m3_value(uint32_t code) {
   const uint32_t m = code & 7, e = (code >> 3) & 15;
   if ((code & 0x7F) == 0x7F) return __longlong_as_double(0x7FF8000000000000ll);
@@ -228,24 +276,70 @@ __device__ __forceinline__ half8 load_half8(const uint16_t* p) {
   return *reinterpret_cast<const half8*>(p);
 }
 
+// x of another lane by a data-parallel move: within four lanes (quad_perm 1 0 3 2
+// and 2 3 0 1), mirrored within eight, within sixteen.
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double moved(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xF, 0xF, false);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+// Over LANES (8 to 64) neighbouring lanes, in every one of them.
+template <int LANES, typename T>
+__device__ __forceinline__ T lanes_sum(T x) {
+  x += moved<0xB1>(x);
+  x += moved<0x4E>(x);
+  x += moved<0x141>(x);
+  if constexpr (LANES >= 16) x += moved<0x140>(x);
+  if constexpr (LANES >= 32) x += __shfl_xor(x, 16);
+  return x;
+}
+__device__ __forceinline__ double wave_max(double x) {
+  x = fmax(x, moved<0xB1>(x));
+  x = fmax(x, moved<0x4E>(x));
+  x = fmax(x, moved<0x141>(x));
+  x = fmax(x, moved<0x140>(x));
+  x = fmax(x, __shfl_xor(x, 16));
+  return fmax(x, __shfl_xor(x, 32));
+}
+
 // T: float for queries, double for keys.  The norm and rotation of eight
 // elements of a head; `lane_at` is the lane's place among the head's LPH.
 // cs: cosines and sines of the lane's own angles.
-template <typename T, int DIM>
-struct Rotor {
-  T c[8], s[8];  // half-split: one per element; interleaved: entries 0 .. 3
-  bool turned;   // the lane's elements are rotated
-
-  __device__ __forceinline__ void angles(const RopeAppendArgs& a, int lane_at, double position) {
+// What a lane needs of the weights and frequencies, for all rows.
+template <int DIM>
+struct Lane {
+  half8 weight;
+  float freq[8];  // of its own angles (interleaved: entries 0 .. 3)
+  bool turned;    // its elements are rotated
+  __device__ __forceinline__ void load(const RopeAppendArgs& a, int lane_at, const uint16_t* w) {
     const int d0 = lane_at * 8, half = a.rot / 2;
+    weight = half8{};
+    if (w) weight = load_half8(w + d0);
     turned = d0 < a.rot;
-    if (!turned) return;
     const int n = a.interleaved ? 4 : 8;
     const int j0 = a.interleaved ? d0 / 2 : d0 < half ? d0 : d0 - half;
 #pragma unroll
+    for (int i = 0; i < 8; ++i) freq[i] = turned && i < n ? a.inv_freq[j0 + i] : 0.0f;
+  }
+};
+
+template <typename T, int DIM>
+struct Rotor {
+  T c[8], s[8];  // half-split: one per element; interleaved: entries 0 .. 3
+
+  __device__ __forceinline__ void angles(const RopeAppendArgs& a, const Lane<DIM>& f, double position) {
+    if (!f.turned) return;
+    const int n = a.interleaved ? 4 : 8;
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (i < n) {
-        const double t = turns_of(position, a.inv_freq[j0 + i]);
+        const double t = turns_of(position, f.freq[i]);
         if constexpr (sizeof(T) == 8) {
           cos_sin_turns(t, &c[i], &s[i]);
         } else {
@@ -259,23 +353,22 @@ struct Rotor {
   }
 
   // x: the raw elements; returns the normed and rotated ones
-  __device__ __forceinline__ void turn(const RopeAppendArgs& a, int lane_at, const half8& x,
-                                       const uint16_t* weight, T out[8]) const {
+  __device__ __forceinline__ void turn(const RopeAppendArgs& a, const Lane<DIM>& f, int lane_at, const half8& x,
+                                       bool normed, T out[8]) const {
     constexpr int LPH = DIM / 8;
     T r = T(1);
-    if (weight) {
+    const bool turned = f.turned;
+    if (normed) {
       T sum = T(0);
 #pragma unroll
       for (int i = 0; i < 8; ++i) sum += (T)x[i] * (T)x[i];
-#pragma unroll
-      for (int d = 1; d < LPH; d <<= 1) sum += __shfl_xor(sum, d);
+      sum = lanes_sum<LPH>(sum);
       if constexpr (sizeof(T) == 8)
         r = 1.0 / sqrt(sum * (1.0 / DIM) + a.eps);
       else
         r = 1.0f / sqrtf(sum * (1.0f / DIM) + (float)a.eps);
-      const half8 w = load_half8(weight + lane_at * 8);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) out[i] = (T)x[i] * r * (T)w[i];
+      for (int i = 0; i < 8; ++i) out[i] = (T)x[i] * r * (T)f.weight[i];
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) out[i] = (T)x[i];
@@ -317,14 +410,15 @@ __device__ __forceinline__ void append_queries(const RopeAppendArgs& a, int wg, 
   uint16_t* const to = a.q_out + row * a.q_stride + lane_at * 8;
   half8 x = {}, next = {};
   if (h0 < a.q_heads) x = load_half8(from + (int64_t)h0 * DIM);
+  Lane<DIM> f;
+  f.load(a, lane_at, a.q_weight);
   Rotor<float, DIM> rotor;
-  rotor.turned = false;
-  if (a.rot) rotor.angles(a, lane_at, (double)a.positions[row]);
+  if (a.rot) rotor.angles(a, f, (double)a.positions[row]);
   for (int i = 0; i < steps; ++i) {
     const int h = h0 + i * HPW;
     if (i + 1 < steps && h + HPW < a.q_heads) next = load_half8(from + (int64_t)(h + HPW) * DIM);
     float out[8];
-    rotor.turn(a, lane_at, x, a.q_weight, out);
+    rotor.turn(a, f, lane_at, x, a.q_weight != nullptr, out);
     half8 y;
 #pragma unroll
     for (int e = 0; e < 8; ++e) y[e] = (_Float16)out[e];
@@ -370,6 +464,8 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   const int near = min(row0 + tid / LPH, a.rows - 1);
   half8 k_near = load_half8(k_from + near * a.qkv_stride), v_near = load_half8(v_from + near * a.qkv_stride);
   int32_t pos_near = a.positions[near];
+  Lane<DIM> f;
+  f.load(a, lane_at, a.k_weight);
   const float scale_k = a.cache.k_scale[block], scale_v = a.cache.v_scale[block];
   u32x4 old[UNITS];
 #pragma unroll
@@ -415,9 +511,8 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
         position = a.positions[t];
       }
       Rotor<double, DIM> rotor;
-      rotor.turned = false;
-      if (a.rot) rotor.angles(a, lane_at, (double)position);
-      rotor.turn(a, lane_at, x, a.k_weight, key[st]);
+      if (a.rot) rotor.angles(a, f, (double)position);
+      rotor.turn(a, f, lane_at, x, a.k_weight != nullptr, key[st]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const double k = fabs(key[st][e]), v = fabs((double)val[st][e]);
@@ -426,11 +521,8 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
       }
     }
   }
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    kmax = fmax(kmax, __shfl_xor(kmax, d));
-    vmax = fmax(vmax, __shfl_xor(vmax, d));
-  }
+  kmax = wave_max(kmax);
+  vmax = wave_max(vmax);
   if (lane == 0) s_max[0][tid >> 6] = kmax, s_max[1][tid >> 6] = vmax;
   __syncthreads();
 #pragma unroll
@@ -442,6 +534,8 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   const double new_k = old_k > need_k ? old_k : need_k, new_v = old_v > need_v ? old_v : need_v;
   const bool grow_k = old_k > 0.0 && new_k > old_k, grow_v = old_v > 0.0 && new_v > old_v;
   const double inv_k = 1.0 / new_k, inv_v = 1.0 / new_v;
+  // (a power of two that FP32 holds with its inverse)
+  const bool plain_v = ((uint64_t)__double_as_longlong(new_v) & 0xFFFFFFFFFFFFFull) == 0 && new_v >= 0x1p-60 && new_v <= 0x1p60;
 
   // keys: 8 codes per lane, two lanes make a 16-byte unit of the layout
   if (grow_k) {
@@ -457,14 +551,10 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
     const int i = st * RPS + tid / LPH;
     if (i < count) {
       const int off = s_list[i], place = ((off >> 2) & 3) * 16 + (off >> 4) * 4 + (off & 3);
-      uint32_t w[2] = {0, 0};
+      const uint2 pair = key_codes(key[st], inv_k), values = value_codes(val[st], inv_v, plain_v);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        w[e >> 2] |= e4m3_code(key[st][e] * inv_k) << (8 * (e & 3));
-        s_v[(lane_at * 8 + e) * kKvPage + place] = (uint8_t)e4m3_code((double)val[st][e] * inv_v);
-      }
-      uint2 pair;
-      pair.x = w[0], pair.y = w[1];
+      for (int e = 0; e < 8; ++e)
+        s_v[(lane_at * 8 + e) * kKvPage + place] = (uint8_t)((e < 4 ? values.x : values.y) >> (8 * (e & 3)));
       *reinterpret_cast<uint2*>(kb + (lane_at >> 1) * (kKvPage * 16) + off * 16 + (lane_at & 1) * 8) = pair;
     }
   }
