@@ -333,16 +333,36 @@ template <typename T, int DIM>
 struct Rotor {
   T c[8], s[8];  // half-split: one per element; interleaved: entries 0 .. 3
 
-  __device__ __forceinline__ void angles(const RopeAppendArgs& a, const Lane<DIM>& f, double position) {
+  __device__ __forceinline__ void angles(const RopeAppendArgs& a, const Lane<DIM>& f, int lane_at, double position) {
     if (!f.turned) return;
-    const int n = a.interleaved ? 4 : 8;
+    if constexpr (sizeof(T) == 8) {
+      if (!a.interleaved) {
+        // the lanes of a pair turn by the same eight angles: each finds four
+        // (64-bit arithmetic is what a page's keys cost) and takes the others
+        const int step = a.rot / 16, lane = threadIdx.x & 63;
+        const bool first = lane_at < step;
+        const int from = first ? lane + step : lane - step;
+        double cc[4], ss[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (i < n) {
-        const double t = turns_of(position, f.freq[i]);
-        if constexpr (sizeof(T) == 8) {
-          cos_sin_turns(t, &c[i], &s[i]);
-        } else {
+        for (int i = 0; i < 4; ++i) cos_sin_turns(turns_of(position, first ? f.freq[i] : f.freq[i + 4]), &cc[i], &ss[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const double oc = __shfl(cc[i], from), os = __shfl(ss[i], from);
+          c[i] = first ? cc[i] : oc;
+          s[i] = first ? ss[i] : os;
+          c[i + 4] = first ? oc : cc[i];
+          s[i + 4] = first ? os : ss[i];
+        }
+        return;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) cos_sin_turns(turns_of(position, f.freq[i]), &c[i], &s[i]);
+    } else {
+      const int n = a.interleaved ? 4 : 8;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (i < n) {
+          const double t = turns_of(position, f.freq[i]);
           // the hardware's functions take turns; their error (below 2^-20) is
           // far under the FP16 step of the result
           c[i] = __builtin_amdgcn_cosf((float)t);
@@ -413,7 +433,7 @@ __device__ __forceinline__ void append_queries(const RopeAppendArgs& a, int wg, 
   Lane<DIM> f;
   f.load(a, lane_at, a.q_weight);
   Rotor<float, DIM> rotor;
-  if (a.rot) rotor.angles(a, f, (double)a.positions[row]);
+  if (a.rot) rotor.angles(a, f, lane_at, (double)a.positions[row]);
   for (int i = 0; i < steps; ++i) {
     const int h = h0 + i * HPW;
     if (i + 1 < steps && h + HPW < a.q_heads) next = load_half8(from + (int64_t)(h + HPW) * DIM);
@@ -511,7 +531,7 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
         position = a.positions[t];
       }
       Rotor<double, DIM> rotor;
-      if (a.rot) rotor.angles(a, f, (double)position);
+      if (a.rot) rotor.angles(a, f, lane_at, (double)position);
       rotor.turn(a, f, lane_at, x, a.k_weight != nullptr, key[st]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
