@@ -111,6 +111,7 @@ int qpn_kv_attention(const qpn_kv_cache* cache, const uint16_t* q, int64_t q_str
   if (q_stride < q_heads * dim || q_stride % 8 != 0 || y_stride < q_heads * dim || y_stride % 4 != 0)
     return QPN_ERR_SHAPE;
   if (rows == 0 || requests == 0) return QPN_OK;
+  if ((int64_t)rows * q_heads > (int64_t(1) << 30)) return QPN_ERR_SHAPE;  // segments are counted in 31 bits
   if (!q || !y || !row_start || !seq_lens || (table_width > 0 && !table)) return QPN_ERR_NULL;
   if (!aligned(q, 16) || !aligned(y, 8) || !aligned(row_start, 4) || !aligned(seq_lens, 4) || !aligned(table, 4) ||
       !aligned(scratch, 16))

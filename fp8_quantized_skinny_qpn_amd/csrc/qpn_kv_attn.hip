@@ -131,7 +131,9 @@ struct Item {
 // P is the smallest of kMinPiecePages or more that makes no more than `target`
 // pieces (to a few steps of bisection for up to 64 requests, by the simple
 // bound for more); everything stays whole when the scratch is too small.
-// Every number fits 31 bits: a call has at most 2^30 rows x query heads.
+// Every number fits 31 bits: a call has at most 2^30 rows x query heads.  (Of
+// requests that name the same rows again and again the count of segments stops
+// at 2^30; item_of turns away what a wrapped total would make.)
 struct Cut {
   int page, total;
 };
@@ -143,7 +145,7 @@ __device__ __forceinline__ Cut cut_of(const AttentionArgs& a, const AttnLaunch& 
       const Req q = request_of(a, l, base + lane);
       my_segs = q.tiles * a.cache.heads;
       my_pages = q.pages;
-      segs += my_segs;
+      segs = min(segs + my_segs, 1 << 24);
       units += (float)my_segs * (float)my_pages;
     }
   }
@@ -234,6 +236,7 @@ __device__ __forceinline__ Item item_of(const AttentionArgs& a, const AttnLaunch
   it.head = (int)((uint32_t)rest / (uint32_t)it.pieces);
   it.piece = rest - it.head * it.pieces;
   it.first = before + (it.head * out.tiles + it.tile) * it.pieces;
+  if (out.tiles == 0 || (uint32_t)it.head >= (uint32_t)heads) it.request = -1;
   return it;
 }
 
@@ -522,6 +525,7 @@ struct Pages {
         id = x;
         kc = a.cache.k_scale[block] * (a.scale * 1.44269504088896340736f);
         vs = a.cache.v_scale[block];
+        if (vs < 0.0f) kc = __builtin_nanf("");  // (the weights of many rows take it as a logarithm)
       }
     }
   }

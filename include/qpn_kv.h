@@ -110,7 +110,8 @@ QPN_API int qpn_kv_plan_round(const int32_t *before, const int32_t *rows, const 
  * FP64 up to their codes, so a code differs from the definition's only where
  * the value is within ~1e-14 of a border between two codes.
  * 0 <= rows <= 2^20, q_heads a multiple of the cache's heads (at most 64 each);
- * eps >= 0.  Alignment: qkv and q_out 16, weights 16, positions, slots 4. */
+ * rows * (q_heads + heads) <= 2^30, eps >= 0.  Alignment: qkv and q_out 16,
+ * weights 16, positions, slots 4. */
 QPN_API int qpn_kv_rope_append(const qpn_kv_cache *cache, const uint16_t *qkv, int64_t qkv_stride,
                                int rows, int q_heads, const uint16_t *q_weight,
                                const uint16_t *k_weight, double eps, const float *inv_freq, int rot,
@@ -132,15 +133,16 @@ QPN_API size_t qpn_kv_attention_scratch_bytes(int requests, int max_rows, int q_
  * q: [rows, q_heads * dim] FP16 (row stride q_stride, a multiple of 8), y the
  * same (row stride y_stride, a multiple of 4).  A row that sees no token gives
  * zeros; what stands in tokens a row does not see (NaN included) never reaches
- * it.  A page number outside the cache gives NaN in the rows that see it, and
- * seq_lens[r] > 64 * table_width gives NaN in all rows of r.  Requests whose
+ * it.  A page number outside the cache, or a page whose values have a negative
+ * scale, gives NaN in the rows that see it, and seq_lens[r] > 64 * table_width
+ * gives NaN in all rows of r.  Requests whose
  * row_start is out of order or past `rows` are skipped; rows of no request are
  * not written.  max_rows: the most rows of one request, a hint that the tile
  * is chosen by.
  * Scores, weights' sums and outputs are held in FP32, the weights are rounded
  * to FP16 for the second product (error 2^-12 of each, averaged over the
  * tokens, next to the output's own 2^-12).  scale > 0, window >= 0.
- * Deterministic.  0 <= rows <= 2^20, requests <= 4096. */
+ * Deterministic.  0 <= rows <= 2^20, rows * q_heads <= 2^30, requests <= 4096. */
 QPN_API int qpn_kv_attention(const qpn_kv_cache *cache, const uint16_t *q, int64_t q_stride,
                              uint16_t *y, int64_t y_stride, int q_heads, int rows, int requests,
                              int max_rows, const int32_t *row_start, const int32_t *seq_lens,
@@ -170,7 +172,8 @@ QPN_API size_t qpn_kv_verify_scratch_bytes(int rows, int requests, int64_t n);
  * gives next = -1; a draft row like that refuses it too, and next comes from
  * p.  A request without rows gives accepted 0, next -1.  All sums and
  * exponentials are FP64.  1 <= n <= 2^24, rows <= 65535, inv_temperature > 0
- * and finite; strides in elements.  One kernel for a greedy drafter, two for a sampled one. */
+ * and finite; strides in elements.  One kernel for a greedy drafter, two for a
+ * sampled one. */
 QPN_API int qpn_kv_verify_sampled(const uint16_t *logits, int64_t logits_stride,
                                   const uint16_t *draft_logits, int64_t draft_stride,
                                   const int32_t *tokens, const int32_t *row_start, int rows,
