@@ -48,14 +48,22 @@ constexpr float kLowest = -3e38f;     // the running maximum before any score
 // wavefronts of a workgroup, few rows: one per 16 dimensions up to eight
 constexpr int few_waves(int dim) { return dim == 64 ? 4 : 8; }
 constexpr int kManyWaves = 8;  // and many rows
+// Pages of a piece at least: one for each of the eight wavefronts of few rows.
+// (8 rows of 40 + 8 heads over 4099 tokens: 20.3 us with 4, 19.0 with 8, 20.8
+// with 16; 256 rows over 4096: 46.3, 46.2, 53.2.)
 constexpr int kMinPiecePages = 8;
-constexpr int kMaxPieces = 1024;   // pieces of a call with cut segments
-constexpr int kJoinDirect = 16;    // pieces joined in one step
+constexpr int kMaxPieces = 512;    // pieces of a call with cut segments
+// Pieces joined in one step.  (8 rows over 16384 tokens, 32 pieces a head: 30.6 us
+// in one step, 26.0 us in two; over 131001 tokens 78.6 and 75.1 us.)
+constexpr int kJoinDirect = 16;
 constexpr int kCounterStep = 8;    // 32-bit words between counters
 static_assert((size_t)kMaxPieces * 2 * kCounterStep * 4 <= kKvZeroedBytes, "two counters per piece");
 
 // The form and the 16-row tiles of a wavefront (of a workgroup, few rows) for
-// `rows` rows of a KV head (query rows x group).
+// `rows` rows of a KV head (query rows x group).  Up to what the registers of
+// the few-rows form hold it is the faster one: 40 rows a head over 4099 / 131001
+// tokens take 19.0 / 75.1 us there and 23.4 / 104 us with many rows' form, 48
+// ragged requests of up to 40 rows 38.8 and 55.5 us.
 constexpr int few_tiles(int dim) { return dim == 256 ? 1 : 3; }   // what the registers hold
 constexpr int many_tiles(int dim) { return dim == 256 ? 1 : 2; }
 struct Form {
@@ -756,6 +764,12 @@ __device__ __forceinline__ void join_pieces(const AttentionArgs& a, const AttnLa
 // nothing is left to join but the weights' sums.  Two buffers: one barrier for W
 // pages.  The next keys are on their way once this page's are used, the next
 // values of a page once its present ones are.
+//
+// Bound: the cache's bytes when there is enough of it (8 rows of 40 + 8 heads of
+// 128 over 131001 tokens, 268 MB, not in any cache: 81.6 us, 3.3 TB/s, where a
+// large copy reaches 4.9; a step of eight pages keeps 128 KiB a CU on its way).
+// Short calls are bound by their chain of dependent steps: launch, table, keys,
+// values, hand-over, join (200 tokens 8.6 us, 4099 tokens 19.0 us).
 // ---------------------------------------------------------------------------
 template <int DIM, int RT>
 struct FewLds {
@@ -1028,6 +1042,10 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
 // ring of kRing pages in LDS (loads straight into it, each wavefront its own
 // part), so that a load has three pages' time to arrive; with the pages of
 // dimension 256 the ring does not fit, and they come through registers.
+//
+// Bound: the matrix and vector units of a SIMD, which two wavefronts share (256
+// rows of 40 + 8 heads of 128 over 20001 tokens, 104 GFLOP: 132 us with the join's
+// 8.8, 790 TFLOP/s, where a large FP16 matrix product reaches 1157).
 // ---------------------------------------------------------------------------
 constexpr int kRing = 4;
 
@@ -1307,9 +1325,13 @@ int64_t most_segments(int requests, int max_rows, int q_heads, int heads, int di
   return (int64_t)requests * heads * (tiles < 1 ? 1 : tiles);
 }
 
-// Pieces wanted: what the chip holds at once (a workgroup a CU), or four times as many and smaller when there are so many segments
-// that whole ones would leave it unevenly loaded.
-int wanted_pieces(int64_t segments) { return segments <= 128 ? 256 : kMaxPieces; }
+// Pieces wanted: what the chip holds at once (a workgroup a CU), or two for each
+// when there are so many segments that whole ones, or the few that can still be
+// cut, would leave it unevenly loaded.  With 256 / 512 pieces, ragged requests of
+// up to 8 rows x 5 query heads: 160 segments of up to 4000 tokens 38 / 48 us, 200 of
+// up to 9000 108 / 78 us, 272 of up to 9000 129 / 103 us, 320 of up to 2000
+// 45 / 48 us; 480 segments of 64 rows 133 / 132 us.
+int wanted_pieces(int64_t segments) { return segments <= 192 ? 256 : kMaxPieces; }
 
 size_t slot_bytes(const Form& f, int dim) { return (size_t)f.rows() * dim * 4 + (size_t)f.rows() * 8; }
 

@@ -16,7 +16,7 @@ namespace {
 // them), kept in LDS, after which every new table entry and every row finds
 // its request by bisection.  The work is a few KiB at most, so the launch and
 // five dependent passes (loads, two scans, bisection, stores) are all there
-// is to pay.
+// is to pay (6.7 us for one request, 7.6 us for 256; an empty launch takes 2.4).
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / kLanes;
@@ -151,6 +151,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_round_kernel(PlanRoundArgs 
 // in: no atomics, no second launch.  Small calls are bound by the chain of
 // dependent loads, so what a page most likely needs (the rows that follow its
 // first one, the old codes) is fetched before it is known to be needed.
+//
+// Bound: one row 8.0 us, 8 rows 7.8 us (40 + 2 x 8 heads of 128): slots, rows,
+// 64-bit angles and codes one after another, of which the angles and norms are
+// 2 us.  1024 rows of prompt blocks: 24 us (27 MB, 1.1 TB/s), where the 64-bit
+// arithmetic of the keys fills 128 CUs for about 12 us beside the queries' 11.
 // ---------------------------------------------------------------------------
 constexpr int kAppendThreads = 256;
 constexpr int kAppendWaves = kAppendThreads / kLanes;
@@ -636,7 +641,8 @@ template <int DIM>
 hipError_t launch_append(const RopeAppendArgs& a) {
   constexpr int HPW = kLanes / (DIM / 8);
   // heads per wavefront: one step of HPW while that leaves fewer wavefronts
-  // than 8 a CU, else more, so that a row's angles serve more heads
+  // than 8 a CU, else more, so that a row's angles serve more heads (1024 rows:
+  // 27.6 us with one step each, 23.6 us so)
   const int groups = (a.q_heads + HPW - 1) / HPW;
   int64_t steps = (int64_t)a.rows * groups / 2048;
   steps = steps < 1 ? 1 : steps > groups ? groups : steps;

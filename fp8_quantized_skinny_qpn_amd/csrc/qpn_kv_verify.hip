@@ -20,6 +20,13 @@
 // finds the token.  Sums run in an order fixed by the sizes, so results are
 // deterministic.
 //
+// Bound: the 64-bit arithmetic of the exponentials (some 20 operations each) next
+// to reading the logits: 32 requests of 8 rows of 151936 tokens, target and
+// drafter (156 MB, 78 million exponentials), take 100 us not in any cache, 70 of
+// them in the first kernel; at a large copy's rate the bytes alone would take 32.
+// 8 rows of a greedy drafter take 16 us: launch, one chunk a workgroup, the joins
+// of the last one and its search are each a chain of dependent steps.
+//
 // What workgroups leave for one another is written through to the device's
 // point of coherence, and lies in 128-byte lines of one request alone: a line
 // that an XCD's L2 holds is never written again by others before it is read.
@@ -38,7 +45,9 @@ constexpr int kArrivalStep = 4;                            // 32-bit words betwe
 static_assert((size_t)kKvMaxRequests * kArrivalStep * 4 <= kKvZeroedBytes, "a counter per request");
 constexpr int kVerifySpan = 64;       // chunks of a workgroup of the first kernel, at most
 constexpr int kVerifyRowsHeld = 16;   // rows of a request whose chunks' masses are held in LDS
-constexpr int kVerifyWgs = 1536;      // workgroups of the first kernel aimed at: the six a CU that its registers let reside
+// Workgroups of the first kernel aimed at: the six a CU that its registers let
+// reside.  (32 x 8 sampled rows of 151936: 97 us with 768, 93 with 1536, 98 with 4096.)
+constexpr int kVerifyWgs = 1536;
 
 // Chunks of a row: rows may start anywhere in a 16-byte granule, so a row's
 // tokens are counted from the granule's start (up to 7 places before it).
