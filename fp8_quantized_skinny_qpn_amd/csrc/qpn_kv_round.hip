@@ -11,12 +11,14 @@ namespace {
 // ---------------------------------------------------------------------------
 // Page tables, slots and positions of a round.
 //
-// One workgroup: two block scans over the requests (pages and rows asked for,
-// which decide admission; then those of the admitted requests, which place
-// them), kept in LDS, after which every new table entry and every row finds
-// its request by bisection.  The work is a few KiB at most, so the launch and
-// five dependent passes (loads, two scans, bisection, stores) are all there
-// is to pay (6.7 us for one request, 7.6 us for 256; an empty launch takes 2.4).
+// One workgroup: a block scan over the requests (pages and rows asked for, which
+// decide admission), a second one only when some are not admitted (then those
+// of the admitted ones place them), kept in LDS, after which every new table
+// entry and every row finds its request by bisection.  The work is a few KiB at
+// most, so the launch and the dependent passes (loads, scan, bisection, stores)
+// are all there is to pay: 6.7 us for one request, 7.0 us for 256, where an empty
+// launch takes 2.4; 31 us for 4096 requests.  (A workgroup of 256 or 512 threads
+// is no faster for one request and slower for more: 7.5 and 7.3 us for 256.)
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / kLanes;
@@ -25,17 +27,24 @@ struct Pair64 {
   int64_t a, b;
 };
 
-__device__ __forceinline__ Pair64 block_inclusive_scan(Pair64 x, Pair64* waves) {
+// The sums up to and including the thread's, and all of them.  Two calls one
+// after the other take different buffers `waves`: then one barrier is enough.
+__device__ __forceinline__ Pair64 block_inclusive_scan(Pair64 x, Pair64* waves, Pair64& total) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) {
     const int64_t a = __shfl_up(x.a, d), b = __shfl_up(x.b, d);
     if (lane >= d) x.a += a, x.b += b;
   }
-  __syncthreads();  // the previous scan's totals have been read
   if (lane == 63) waves[wave] = x;
   __syncthreads();
-  for (int w = 0; w < wave; ++w) x.a += waves[w].a, x.b += waves[w].b;
+  total = {0, 0};
+#pragma unroll
+  for (int w = 0; w < kPlanWaves; ++w) {
+    const Pair64 o = waves[w];
+    if (w < wave) x.a += o.a, x.b += o.b;
+    total.a += o.a, total.b += o.b;
+  }
   return x;
 }
 
@@ -52,8 +61,7 @@ __device__ __forceinline__ int bisect(const int32_t* start, int n, int32_t x) {
 __global__ __launch_bounds__(kPlanThreads) void plan_round_kernel(PlanRoundArgs a) {
   __shared__ int32_t s_row[kKvMaxRequests + 1];   // first row of each request
   __shared__ int32_t s_take[kKvMaxRequests + 1];  // pages taken before each request
-  __shared__ Pair64 s_waves[kPlanWaves];
-  __shared__ Pair64 s_carry;
+  __shared__ Pair64 s_waves[2][kPlanWaves];
   const int tid = threadIdx.x;
   const int chunks = (a.requests + kPlanThreads - 1) / kPlanThreads;
   int64_t free_count = *a.free_count;
@@ -78,28 +86,28 @@ __global__ __launch_bounds__(kPlanThreads) void plan_round_kernel(PlanRoundArgs 
   };
 
   Pair64 asked_before{0, 0}, placed_before{0, 0};  // totals of the former chunks
+  int buffer = 0;
   for (int c = 0; c < chunks; ++c) {
     const int r = c * kPlanThreads + tid;
     const Asked q = asked_of(r);
-    Pair64 up = block_inclusive_scan({q.want, q.rows}, s_waves);
-    up.a += asked_before.a, up.b += asked_before.b;
-    const bool go = q.fine && up.a <= free_count && up.b <= a.capacity;
-    if (tid == kPlanThreads - 1) s_carry = up;
-    const Pair64 mine{go ? q.want : 0, go ? q.rows : 0};
-    Pair64 at = block_inclusive_scan(mine, s_waves);  // (its barriers publish s_carry)
-    asked_before = s_carry;
+    Pair64 mine{q.want, q.rows}, total;
+    Pair64 at = block_inclusive_scan(mine, s_waves[buffer], total);
+    buffer ^= 1;
+    const bool go = q.fine && asked_before.a + at.a <= free_count && asked_before.b + at.b <= a.capacity;
+    asked_before.a += total.a, asked_before.b += total.b;
+    if (asked_before.a > free_count || asked_before.b > a.capacity) {  // some are not admitted
+      if (!go) mine = {0, 0};
+      at = block_inclusive_scan(mine, s_waves[buffer], total);
+      buffer ^= 1;
+    }
     at.a += placed_before.a, at.b += placed_before.b;
+    placed_before.a += total.a, placed_before.b += total.b;
     if (r < a.requests) {
       s_row[r] = (int32_t)(at.b - mine.b);
       s_take[r] = (int32_t)(at.a - mine.a);
       a.row_start[r] = (int32_t)(at.b - mine.b);
       a.seq_lens[r] = q.fine ? (int32_t)(q.before + mine.b) : 0;
     }
-    __syncthreads();  // s_carry has been read
-    if (tid == kPlanThreads - 1) s_carry = at;
-    __syncthreads();
-    placed_before = s_carry;
-    __syncthreads();
   }
   const int32_t pages = (int32_t)placed_before.a, rows = (int32_t)placed_before.b;
   if (tid == 0) {
