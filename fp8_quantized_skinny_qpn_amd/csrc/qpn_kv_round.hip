@@ -162,11 +162,10 @@ __global__ __launch_bounds__(kPlanThreads) void plan_round_kernel(PlanRoundArgs 
 //
 // Bound: one row 8.0 us, 8 rows 7.8 us (40 + 2 x 8 heads of 128): slots, rows,
 // 64-bit angles and codes one after another, of which the angles and norms are
-// 2 us.  1024 rows of prompt blocks: 24 us (27 MB, 1.1 TB/s), where the 64-bit
-// arithmetic of the keys fills 128 CUs for about 12 us beside the queries' 11.
+// 2 us.  4 x 256 rows of prompt blocks: 20 us (27 MB, 1.4 TB/s), the 64-bit
+// arithmetic of the keys (for about 10 us) beside the queries' 11.
 // ---------------------------------------------------------------------------
-constexpr int kAppendThreads = 256;
-constexpr int kAppendWaves = kAppendThreads / kLanes;
+constexpr int kValuePitch = kKvPage + 4;
 
 // pos * f / (2 pi) less its nearest whole number, in turns.  The product of a
 // 31-bit position and a 24-bit frequency is rounded once; 1 / (2 pi) is taken
@@ -430,12 +429,12 @@ struct Rotor {
   }
 };
 
-template <int DIM>
+template <int DIM, int THREADS>
 __device__ __forceinline__ void append_queries(const RopeAppendArgs& a, int wg, int waves_per_row,
                                                int steps) {
   constexpr int LPH = DIM / 8, HPW = kLanes / LPH;
   const int lane = threadIdx.x & 63, lane_at = lane % LPH;
-  const int64_t wave = (int64_t)wg * kAppendWaves + (threadIdx.x >> 6);
+  const int64_t wave = (int64_t)wg * (THREADS / kLanes) + (threadIdx.x >> 6);
   const int64_t row = wave / waves_per_row;
   if (row >= a.rows) return;  // a whole wavefront; no barrier follows
   const int h0 = (int)(wave % waves_per_row) * steps * HPW + lane / LPH;
@@ -473,17 +472,19 @@ __device__ __forceinline__ u32x4 recode16(u32x4 c, double ratio) {
   return o;
 }
 
-template <int DIM>
+template <int DIM, int THREADS>
 __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, int32_t slot0, int head) {
   constexpr int LPH = DIM / 8;
-  constexpr int RPS = kAppendThreads / LPH;  // rows a step of the workgroup takes
+  constexpr int RPS = THREADS / LPH;  // rows a step of the workgroup takes
   constexpr int STEPS = kKvPage / RPS;
-  constexpr int UNITS = DIM * 4 / kAppendThreads;  // 16-byte units of the values' block, of a thread
+  constexpr int UNITS = (DIM * 4 + THREADS - 1) / THREADS;  // 16-byte units of the values' block, of a thread
   __shared__ int32_t s_row[kKvPage];      // the row at each offset of the page, -1: none
   __shared__ int32_t s_list[kKvPage];     // the offsets that are written, in order
   __shared__ int32_t s_earlier, s_count;
-  __shared__ double s_max[2][kAppendWaves];
-  __shared__ __attribute__((aligned(16))) uint8_t s_v[DIM * kKvPage];
+  __shared__ uint64_t s_taken;            // bit o: offset o is written
+  __shared__ double s_max[2][THREADS / kLanes];
+  // new values' codes; dimensions 68 bytes apart, so that the lanes of a row meet different banks
+  __shared__ __attribute__((aligned(16))) uint8_t s_v[DIM * kValuePitch];
   const int tid = threadIdx.x, lane = tid & 63, lane_at = tid % LPH;
 
   const int32_t page = slot0 / kKvPage;
@@ -502,12 +503,15 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   const float scale_k = a.cache.k_scale[block], scale_v = a.cache.v_scale[block];
   u32x4 old[UNITS];
 #pragma unroll
-  for (int i = 0; i < UNITS; ++i) old[i] = *reinterpret_cast<const u32x4*>(vb + (tid + i * kAppendThreads) * 16);
+  for (int i = 0; i < UNITS; ++i) {
+    old[i] = u32x4{0, 0, 0, 0};
+    if (tid + i * THREADS < DIM * 4) old[i] = *reinterpret_cast<const u32x4*>(vb + (tid + i * THREADS) * 16);
+  }
 
   if (tid < kKvPage) s_row[tid] = -1;
   if (tid == 0) s_earlier = 0;
   __syncthreads();
-  for (int t = tid; t < a.rows; t += kAppendThreads) {
+  for (int t = tid; t < a.rows; t += THREADS) {
     const int32_t s = a.slots[t];
     if (s >= 0 && s / kKvPage == page) {
       if (t < row0) s_earlier = 1;
@@ -519,7 +523,7 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   if (tid < kKvPage) {
     const uint64_t taken = __ballot(s_row[tid] >= 0);
     if (s_row[tid] >= 0) s_list[__popcll(taken & ((1ull << tid) - 1))] = tid;
-    if (tid == 0) s_count = __popcll(taken);
+    if (tid == 0) s_count = __popcll(taken), s_taken = taken;
   }
   __syncthreads();
   const int count = s_count;
@@ -559,7 +563,7 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   if (lane == 0) s_max[0][tid >> 6] = kmax, s_max[1][tid >> 6] = vmax;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kAppendWaves; ++w) {
+  for (int w = 0; w < (THREADS / kLanes); ++w) {
     kmax = fmax(kmax, s_max[0][w]);
     vmax = fmax(vmax, s_max[1][w]);
   }
@@ -573,7 +577,7 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   // keys: 8 codes per lane, two lanes make a 16-byte unit of the layout
   if (grow_k) {
     const double ratio = old_k / new_k;
-    for (int u = tid; u < (DIM / 16) * kKvPage; u += kAppendThreads) {
+    for (int u = tid; u < (DIM / 16) * kKvPage; u += THREADS) {
       if (s_row[u % kKvPage] >= 0) continue;
       u32x4* p = reinterpret_cast<u32x4*>(kb + u * 16);
       *p = recode16(*p, ratio);
@@ -587,7 +591,7 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
       const uint2 pair = key_codes(key[st], inv_k), values = value_codes(val[st], inv_v, plain_v);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        s_v[(lane_at * 8 + e) * kKvPage + place] = (uint8_t)((e < 4 ? values.x : values.y) >> (8 * (e & 3)));
+        s_v[(lane_at * 8 + e) * kValuePitch + place] = (uint8_t)((e < 4 ? values.x : values.y) >> (8 * (e & 3)));
       *reinterpret_cast<uint2*>(kb + (lane_at >> 1) * (kKvPage * 16) + off * 16 + (lane_at & 1) * 8) = pair;
     }
   }
@@ -595,14 +599,19 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
 
   // values: 16-byte segments (dimension d, group g) of the tokens 16 t + 4 g + r
   const double ratio_v = grow_v ? old_v / new_v : 1.0;
+  const uint64_t taken = s_taken;
 #pragma unroll
   for (int i = 0; i < UNITS; ++i) {
-    const int u = tid + i * kAppendThreads, g = u & 3;
-    uint32_t fresh_bytes = 0;  // bit 4 t + r: token 16 t + 4 g + r is new
-#pragma unroll
-    for (int j = 0; j < 16; ++j) fresh_bytes |= (uint32_t)(s_row[(j >> 2) * 16 + g * 4 + (j & 3)] >= 0) << j;
+    const int u = tid + i * THREADS, g = u & 3;
+    if (u >= DIM * 4) break;
+    // bit 4 t + r: token 16 t + 4 g + r is new
+    const uint64_t mine = taken >> (4 * g);
+    const uint32_t fresh_bytes = (uint32_t)(mine & 15) | (uint32_t)(mine >> 12 & 0xF0) | (uint32_t)(mine >> 24 & 0xF00) |
+                                 (uint32_t)(mine >> 36 & 0xF000);
     if (!fresh_bytes && !grow_v) continue;
-    u32x4 c = *reinterpret_cast<const u32x4*>(s_v + u * 16);
+    u32x4 c;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) c[t] = *reinterpret_cast<const uint32_t*>(s_v + (u >> 2) * kValuePitch + g * 16 + t * 4);
     if (fresh_bytes != 0xFFFFu) {
       u32x4 o = old[i];
       if (grow_v) o = recode16(o, ratio_v);
@@ -622,47 +631,72 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   }
 }
 
-// The pages that rows row0 .. row0 + rows - 1 begin runs of (rows that follow one
-// another on one page).
-template <int DIM>
+// The pages that rows row0 .. row0 + rows - 1 (at most 64) begin runs of (rows that
+// follow one another on one page).
+template <int DIM, int THREADS>
 __device__ __forceinline__ void append_rows(const RopeAppendArgs& a, int row0, int rows, int head) {
   const int64_t places = a.cache.pages * kKvPage;
-  for (int t = row0; t < min(row0 + rows, a.rows); ++t) {  // (the whole workgroup agrees)
-    const int32_t slot = a.slots[t], before = t > 0 ? a.slots[t - 1] : -1;
-    if (slot < 0 || slot >= places) continue;
-    if (before >= 0 && before / kKvPage == slot / kKvPage) continue;
-    append_page<DIM>(a, t, slot, head);
+  const int lane = threadIdx.x & 63, t = row0 + lane;
+  int32_t slot = -1, before = -1;
+  if (lane < rows && t < a.rows) {
+    slot = a.slots[t];
+    if (t > 0) before = a.slots[t - 1];
+  }
+  const bool starts = slot >= 0 && slot < places && !(before >= 0 && before / kKvPage == slot / kKvPage);
+  for (uint64_t left = __ballot(starts); left; left &= left - 1) {  // (every wavefront finds the same)
+    const int i = __ffsll((unsigned long long)left) - 1;
+    append_page<DIM, THREADS>(a, row0 + i, __builtin_amdgcn_readlane(slot, i), head);
     if (rows > 1) __syncthreads();  // its LDS has been read
   }
 }
 
-template <int DIM>
-__global__ __launch_bounds__(kAppendThreads) void rope_append_kernel(RopeAppendArgs a, int cache_wgs, int rows_per_wg,
-                                                                     int waves_per_row, int steps) {
-  if ((int)blockIdx.x < cache_wgs)
-    append_rows<DIM>(a, (int)blockIdx.x / a.cache.heads * rows_per_wg, rows_per_wg, (int)blockIdx.x % a.cache.heads);
-  else
-    append_queries<DIM>(a, (int)blockIdx.x - cache_wgs, waves_per_row, steps);
+// Cache workgroup w: KV head w % heads of a block of rows_per_wg rows.  Pages of
+// long runs begin in every kKvPage / rows_per_wg'th block; `groups` blocks so far
+// apart come one after the other, so that those which have work do not all fall
+// to the same few CUs.
+template <int DIM, int THREADS>
+__global__ __launch_bounds__(THREADS) void rope_append_kernel(RopeAppendArgs a, int cache_wgs, int rows_per_wg,
+                                                              int groups, int waves_per_row, int steps) {
+  if ((int)blockIdx.x < cache_wgs) {
+    const int at = (int)blockIdx.x / a.cache.heads, apart = kKvPage / rows_per_wg;
+    const int block = rows_per_wg == 1 ? at : at % groups * apart + at / groups;
+    append_rows<DIM, THREADS>(a, block * rows_per_wg, rows_per_wg, (int)blockIdx.x % a.cache.heads);
+  } else {
+    append_queries<DIM, THREADS>(a, (int)blockIdx.x - cache_wgs, waves_per_row, steps);
+  }
 }
 
-template <int DIM>
-hipError_t launch_append(const RopeAppendArgs& a) {
-  constexpr int HPW = kLanes / (DIM / 8);
+template <int DIM, int THREADS>
+hipError_t launch_append(const RopeAppendArgs& a, int rows_per_wg) {
+  constexpr int HPW = kLanes / (DIM / 8), WAVES = THREADS / kLanes;
   // heads per wavefront: one step of HPW while that leaves fewer wavefronts
   // than 8 a CU, else more, so that a row's angles serve more heads (1024 rows:
   // 27.6 us with one step each, 23.6 us so)
-  const int groups = (a.q_heads + HPW - 1) / HPW;
-  int64_t steps = (int64_t)a.rows * groups / 2048;
-  steps = steps < 1 ? 1 : steps > groups ? groups : steps;
-  const int waves_per_row = (int)((groups + steps - 1) / steps);
-  // rows of a cache workgroup: one while those of all rows are on the chip at
-  // once, else so many that most workgroups have a page to do
-  const int rows_per_wg = (int64_t)a.rows * a.cache.heads <= 2048 ? 1 : 16;
-  const int64_t cache_wgs = (int64_t)((a.rows + rows_per_wg - 1) / rows_per_wg) * a.cache.heads;
-  const int64_t query_wgs = ((int64_t)a.rows * waves_per_row + kAppendWaves - 1) / kAppendWaves;
-  rope_append_kernel<DIM><<<dim3((uint32_t)(cache_wgs + query_wgs)), dim3(kAppendThreads), 0,
-                            (hipStream_t)a.stream>>>(a, (int)cache_wgs, rows_per_wg, waves_per_row, (int)steps);
+  const int head_groups = (a.q_heads + HPW - 1) / HPW;
+  int64_t steps = (int64_t)a.rows * head_groups / 2048;
+  steps = steps < 1 ? 1 : steps > head_groups ? head_groups : steps;
+  const int waves_per_row = (int)((head_groups + steps - 1) / steps);
+  const int groups = rows_per_wg == 1 ? a.rows : (a.rows + kKvPage - 1) / kKvPage;
+  const int64_t cache_wgs = (int64_t)groups * (rows_per_wg == 1 ? 1 : kKvPage / rows_per_wg) * a.cache.heads;
+  const int64_t query_wgs = ((int64_t)a.rows * waves_per_row + WAVES - 1) / WAVES;
+  rope_append_kernel<DIM, THREADS><<<dim3((uint32_t)(cache_wgs + query_wgs)), dim3(THREADS), 0, (hipStream_t)a.stream>>>(
+      a, (int)cache_wgs, rows_per_wg, groups, waves_per_row, (int)steps);
   return hipGetLastError();
+}
+
+// Rows of a cache workgroup: one while those of all rows are about what the chip
+// holds at once, since each row may have a page of its own (64 requests of one
+// row and 8 heads: 10 us; with 16 rows a workgroup 78).  Above that many rows follow
+// others on their pages and most workgroups of one row would only look and
+// leave: eight (1024 prompt rows of one request: 31.6 us with one, 17.7 with four,
+// 15.8 with eight, 15.7 with 16; 300 requests of one row 43.7 us with four, 50.7
+// with eight, 79.7 with 16).  Pages of 256 dimensions then take eight wavefronts (2 x
+// 512 rows of 16 + 2 x 8 heads: 59.6 us with four, 40.1 with eight), the others four
+// (1024 rows of 128 dimensions: 15.9 and 17.4).
+template <int DIM>
+hipError_t launch_append(const RopeAppendArgs& a) {
+  if ((int64_t)a.rows * a.cache.heads <= 2048) return launch_append<DIM, 256>(a, 1);
+  return launch_append<DIM, DIM == 256 ? 512 : 256>(a, 8);
 }
 
 }  // namespace
