@@ -78,7 +78,10 @@ int qpn_kv_rope_append(const qpn_kv_cache* cache, const uint16_t* qkv, int64_t q
       q_stride < q_heads * dim || q_stride % 8 != 0)
     return QPN_ERR_SHAPE;
   if (rows == 0) return QPN_OK;
-  if ((int64_t)rows * (cache->heads + q_heads) > (int64_t(1) << 30)) return QPN_ERR_SHAPE;  // workgroups
+  // a launch has less than 2^32 threads: those of the cache are up to 64 for a row and head
+  if ((int64_t)rows * (cache->heads + q_heads) > (int64_t(1) << 30) ||
+      (int64_t)rows * cache->heads > (int64_t(1) << 25))
+    return QPN_ERR_SHAPE;
   if (!qkv || !q_out || !positions || !slots || (rot > 0 && !inv_freq)) return QPN_ERR_NULL;
   if (!aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) ||
       !aligned(inv_freq, 4) || !aligned(positions, 4) || !aligned(slots, 4))

@@ -110,8 +110,8 @@ QPN_API int qpn_kv_plan_round(const int32_t *before, const int32_t *rows, const 
  * FP64 up to their codes, so a code differs from the definition's only where
  * the value is within ~1e-14 of a border between two codes.
  * 0 <= rows <= 2^20, q_heads a multiple of the cache's heads (at most 64 each);
- * rows * (q_heads + heads) <= 2^30, eps >= 0.  Alignment: qkv and q_out 16,
- * weights 16, positions, slots 4. */
+ * rows * (q_heads + heads) <= 2^30, rows * heads <= 2^25, eps >= 0.  Alignment:
+ * qkv and q_out 16, weights 16, positions, slots 4. */
 QPN_API int qpn_kv_rope_append(const qpn_kv_cache *cache, const uint16_t *qkv, int64_t qkv_stride,
                                int rows, int q_heads, const uint16_t *q_weight,
                                const uint16_t *k_weight, double eps, const float *inv_freq, int rot,

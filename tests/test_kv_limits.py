@@ -34,6 +34,9 @@ def test_append_bounds_rows_times_heads(kv):
     call = lambda rows: kv.lib.qpn_kv_rope_append(  # noqa: E731
         cache(kv, 512), P, s, rows, 1024, None, None, 1e-6, P, 64, 0, P, P, P, 1024 * 64, None)
     assert call((1 << 30) // 1536 + 1) == SHAPE
+    assert call((1 << 25) // 512 + 1) == SHAPE
+    if not torch.cuda.is_available():
+        assert call((1 << 25) // 512) == DEVICE
     assert call(0) == 0
 
 
