@@ -16,9 +16,10 @@ namespace {
 // of the admitted ones place them), kept in LDS, after which every new table
 // entry and every row finds its request by bisection.  The work is a few KiB at
 // most, so the launch and the dependent passes (loads, scan, bisection, stores)
-// are all there is to pay: 6.7 us for one request, 7.0 us for 256, where an empty
-// launch takes 2.4; 31 us for 4096 requests.  (A workgroup of 256 or 512 threads
-// is no faster for one request and slower for more: 7.5 and 7.3 us for 256.)
+// are all there is to pay: 4.6 us for one request, 6.6 us for 256 (from a graph; an
+// empty launch takes 2.4), 31 us for 4096 requests.  (A workgroup of 256 or 512 threads
+// is no faster for one request and slower for more: on a stream 7.5 and 7.3 us for
+// 256, against 7.0.)
 // ---------------------------------------------------------------------------
 constexpr int kPlanThreads = 1024;
 constexpr int kPlanWaves = kPlanThreads / kLanes;
@@ -670,8 +671,8 @@ template <int DIM, int THREADS>
 hipError_t launch_append(const RopeAppendArgs& a, int rows_per_wg) {
   constexpr int HPW = kLanes / (DIM / 8), WAVES = THREADS / kLanes;
   // heads per wavefront: one step of HPW while that leaves fewer wavefronts
-  // than 8 a CU, else more, so that a row's angles serve more heads (1024 rows:
-  // 27.6 us with one step each, 23.6 us so)
+  // than 8 a CU, else more, so that a row's angles serve more heads (1024 rows of
+  // one request: 18.1 us with one step each, 15.7 us so; 257 x 8 rows 58.4 and 49.9)
   const int head_groups = (a.q_heads + HPW - 1) / HPW;
   int64_t steps = (int64_t)a.rows * head_groups / 2048;
   steps = steps < 1 ? 1 : steps > head_groups ? head_groups : steps;
