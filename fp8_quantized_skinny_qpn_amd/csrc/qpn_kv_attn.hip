@@ -603,10 +603,11 @@ __device__ __forceinline__ void write_y(const AttentionArgs& a, const AttnLaunch
   const int row = row_of(l, rr);
   half4 h;
   float inverse = 1.0f / weight;
-  if (weight == 0.0f) {
-    // nothing seen gives zeros; tokens seen but no weight (every score -inf) has no value
+  if (weight == 0.0f || q.bad) {
+    // nothing seen gives zeros; tokens seen but no weight (every score -inf) has no value, and
+    // neither has a row of a request longer than its table (whose rows' places are not known)
     sum = float4v{0, 0, 0, 0};
-    inverse = q.seq - q.rows + row + 1 > 0 ? __builtin_nanf("") : 0.0f;
+    inverse = q.bad || q.seq - q.rows + row + 1 > 0 ? __builtin_nanf("") : 0.0f;
   }
 #pragma unroll
   for (int e = 0; e < 4; ++e) h[e] = (_Float16)(sum[e] * inverse);
