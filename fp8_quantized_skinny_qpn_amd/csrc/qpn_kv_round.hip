@@ -220,7 +220,17 @@ __device__ __forceinline__ uint32_t e4m3_code(double x) {
   return sign | (uint32_t)((e + 7) * 8 + (int)rint(a * inv_step) - 8);
 }
 
-// Eight values times inv as E4M3 codes (byte e: element e).  The gfx950
+// A page's scale, as new codes are divided by it.  By a power of two that is a
+// product with its inverse; another one (a caller's, kept by a page) is divided
+// by, since a product with a rounded inverse misses values halfway between codes.
+struct PageScale {
+  double value, inverse;
+  bool power_of_two;
+  __device__ __forceinline__ explicit PageScale(double s)
+      : value(s), inverse(1.0 / s), power_of_two(((uint64_t)__double_as_longlong(s) & 0xFFFFFFFFFFFFFull) == 0) {}
+};
+
+// Eight values as E4M3 codes (byte e: element e).  The gfx950
 // conversion rounds FP32 correctly; what FP32 holds exactly goes through it.
 __device__ __forceinline__ float clamp448(float x) {  // (a NaN stays)
   return x > 448.0f ? 448.0f : x < -448.0f ? -448.0f : x;
@@ -232,28 +242,36 @@ __device__ __forceinline__ uint2 pack_codes(const float f[8]) {
   hi = __builtin_amdgcn_cvt_pk_fp8_f32(clamp448(f[6]), clamp448(f[7]), hi, true);
   return make_uint2((uint32_t)lo, (uint32_t)hi);
 }
-// FP16 values: a product with a power of two is exact, another scale goes
-// through 64 bits.
-__device__ __forceinline__ uint2 value_codes(const half8& x, double inv, bool power_of_two) {
-  if (power_of_two) {
+// FP16 values: a product with a power of two (that FP32 holds with its inverse)
+// is exact, another scale goes through 64 bits.
+__device__ __forceinline__ uint2 value_codes(const half8& x, const PageScale& s) {
+  if (s.power_of_two && s.value <= 0x1p60) {  // (no scale is below 2^-60)
     float f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = (float)x[e] * (float)inv;
+    for (int e = 0; e < 8; ++e) f[e] = (float)x[e] * (float)s.inverse;
     return pack_codes(f);
   }
   uint32_t w[2] = {0, 0};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e >> 2] |= e4m3_code((double)x[e] * inv) << (8 * (e & 3));
+  for (int e = 0; e < 8; ++e) w[e >> 2] |= e4m3_code((double)x[e] / s.value) << (8 * (e & 3));
   return make_uint2(w[0], w[1]);
 }
 // Keys: their FP32 rounding goes the same way unless it lies on a border
 // between two codes (or among the subnormal ones, whose borders lie closer).
-__device__ __forceinline__ uint2 key_codes(const double x[8], double inv) {
+__device__ __forceinline__ uint2 key_codes(const double x[8], const PageScale& s) {
+  double q[8];
   float f[8];
   bool near = false;
+  if (s.power_of_two) {  // (one branch for all of them)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = x[e] * s.inverse;
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[e] = x[e] / s.value;
+  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    f[e] = (float)(x[e] * inv);
+    f[e] = (float)q[e];
     near |= (__builtin_bit_cast(uint32_t, f[e]) & 0xFFFFFu) == 0x80000u || fabsf(f[e]) < 0x1p-6f;
   }
   uint2 w = pack_codes(f);
@@ -261,7 +279,7 @@ __device__ __forceinline__ uint2 key_codes(const double x[8], double inv) {
     w = make_uint2(0, 0);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const uint32_t c = e4m3_code(x[e] * inv) << (8 * (e & 3));
+      const uint32_t c = e4m3_code(q[e]) << (8 * (e & 3));
       if (e < 4) w.x |= c; else w.y |= c;
     }
   }
@@ -571,9 +589,7 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
   const double need_k = page_scale_for(kmax), need_v = page_scale_for(vmax);
   const double new_k = old_k > need_k ? old_k : need_k, new_v = old_v > need_v ? old_v : need_v;
   const bool grow_k = old_k > 0.0 && new_k > old_k, grow_v = old_v > 0.0 && new_v > old_v;
-  const double inv_k = 1.0 / new_k, inv_v = 1.0 / new_v;
-  // (a power of two that FP32 holds with its inverse)
-  const bool plain_v = ((uint64_t)__double_as_longlong(new_v) & 0xFFFFFFFFFFFFFull) == 0 && new_v >= 0x1p-60 && new_v <= 0x1p60;
+  const PageScale by_k(new_k), by_v(new_v);
 
   // keys: 8 codes per lane, two lanes make a 16-byte unit of the layout
   if (grow_k) {
@@ -589,7 +605,7 @@ __device__ __forceinline__ void append_page(const RopeAppendArgs& a, int row0, i
     const int i = st * RPS + tid / LPH;
     if (i < count) {
       const int off = s_list[i], place = ((off >> 2) & 3) * 16 + (off >> 4) * 4 + (off & 3);
-      const uint2 pair = key_codes(key[st], inv_k), values = value_codes(val[st], inv_v, plain_v);
+      const uint2 pair = key_codes(key[st], by_k), values = value_codes(val[st], by_v);
 #pragma unroll
       for (int e = 0; e < 8; ++e)
         s_v[(lane_at * 8 + e) * kValuePitch + place] = (uint8_t)((e < 4 ? values.x : values.y) >> (8 * (e & 3)));

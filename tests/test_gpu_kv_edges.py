@@ -5,8 +5,9 @@ References and tolerances are those of test_gpu_kv.py; where one differs it is d
 import numpy as np
 import pytest
 
+import kv_ref
 from gpu_util import need_gpu
-from test_gpu_kv import PAGE, AttnCase
+from test_gpu_kv import PAGE, AttnCase, append_case, run_slots
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +41,32 @@ def test_attention_more_rows_than_the_table_has_places(kv, dim, hq, hk, rows, to
     # alone, the call's work is cut in another way
     c.q, c.row_start, c.seq, c.table, c.lens = c.q[2:2 + rows], np.array([0, rows]), [tokens], c.table[1:2], c.lens[1:2]
     assert np.isnan(c.run()).all()
+
+
+# ---------------------------------------------------------------- rope_append
+
+def halfway_values(scale):
+    """The FP16 values x > 0 with x / scale halfway between two E4M3 values (exactly, in 64 bits)."""
+    x = np.arange(1, 0x7C00, dtype=np.uint16).view(np.float16).astype(np.float64)
+    x = x[x <= 224]                                # (larger ones would raise a scale between 1/2 and 1)
+    return x[np.isin(x / scale, (kv_ref.VALUES[1:127] + kv_ref.VALUES[:126]) / 2)]
+
+
+@pytest.mark.parametrize("scale", [0.8046875, 0.8359375, 0.9140625, 0.9609375, 0.92578125])
+def test_append_ties_of_scales_that_are_no_power_of_two(kv, scale):
+    # a page keeps its former scale s, of any 24 bits; a value halfway between two codes goes to the
+    # even one, which x * (1 / s) misses where that product is rounded off the middle
+    ties = halfway_values(scale)
+    off = kv_ref.e4m3_codes(ties / scale) != kv_ref.e4m3_codes(ties * (1.0 / scale))
+    assert off.any()
+    rows, hq, hk, dim = 3, 2, 1, 64
+    x = np.resize(ties, (rows, (hq + 2 * hk) * dim)) * np.where(np.arange(rows) % 2, -1.0, 1.0)[:, None]
+    x[2, (hq + hk) * dim] = np.inf                 # saturates
+    x[2, (hq + hk) * dim + 1] = np.nan
+    append_case(kv, dim, hq, hk, [5, 6, 17], [5, 6, 17], 1, 51, rot=0, norm=False, x=x.astype(np.float16), old=scale)
+
+
+def test_append_odd_scales_of_rotated_keys(kv):
+    slots, pos = run_slots([(1000, 300), (70, 30), (63, 66)], 14, 52)
+    for old in (0.0123, 0.7, 37.3):
+        append_case(kv, 128, 4, 2, slots, pos, 14, 53, old=old)
