@@ -258,13 +258,17 @@ __device__ __forceinline__ half8 to_half8(const float4v& a, const float4v& b) {
   return h;
 }
 
+// The first token that a row sees which sees those below lim.  (lim is negative
+// for rows before the first token: no difference is taken below the window.)
+__device__ __forceinline__ int low_of(int lim, int window) { return window > 0 && lim > window ? lim - window : 0; }
+
 // What the rows of a wavefront see: tokens [low, lim) of the lane's row of
 // each tile, and the extremes over its rows.
 template <int RT>
 struct View {
   int lim[RT], window;
   int lim_min, lim_max, low_min, low_max;
-  __device__ __forceinline__ int low(int rt) const { return window > 0 ? max(0, lim[rt] - window) : 0; }
+  __device__ __forceinline__ int low(int rt) const { return low_of(lim[rt], window); }
 };
 
 // Bits of the tokens [low, lim) among the 32 from `base` on, from the lane's
@@ -558,8 +562,8 @@ __device__ __forceinline__ View<RT> view_of(const AttentionArgs& a, const AttnLa
     v.lim[t] = t * 16 + c16 < rows ? at + row_of(l, first + t * 16 + c16) : 0;
   v.lim_min = uniform(at + row_of(l, first));
   v.lim_max = uniform(at + row_of(l, first + rows - 1));
-  v.low_min = a.window > 0 ? max(0, v.lim_min - a.window) : 0;
-  v.low_max = a.window > 0 ? max(0, v.lim_max - a.window) : 0;
+  v.low_min = low_of(v.lim_min, a.window);
+  v.low_max = low_of(v.lim_max, a.window);
   return v;
 }
 

@@ -43,6 +43,19 @@ def test_attention_more_rows_than_the_table_has_places(kv, dim, hq, hk, rows, to
     assert np.isnan(c.run()).all()
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[(5, 3), (4, 0), (2, 100), (3, 1)], [(70, 3), (60, 0), (50, 100), (90, 70)], [(8, 3)],
+                                  [(300, 200)]])
+def test_attention_windows_of_rows_before_the_first_token(kv, dim, lens):
+    # fewer tokens than rows, and windows up to the widest: from the tokens' number on a window hides nothing
+    c = AttnCase(kv, lens, 4, 2, dim, 54)
+    clean = c.run()
+    c.check(clean)
+    c.check(c.run(window=1), 1)
+    for window in (2 ** 31 - 1, 2 ** 31 - 2, 2 ** 31 - 200, 2 ** 30):
+        assert np.array_equal(c.run(window=window), clean), window
+
+
 # ---------------------------------------------------------------- rope_append
 
 def halfway_values(scale):
