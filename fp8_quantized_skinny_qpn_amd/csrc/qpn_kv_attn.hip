@@ -342,7 +342,7 @@ struct Rows {
       for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
         for (int d = 0; d < DT; ++d) o[d][rt] *= f;
-    } else if (vs <= vref * kScaleLeast) {  // (a NaN goes on)
+    } else if (vs <= vref * kScaleLeast) {
       vs = vref;
       return false;
     }
@@ -537,7 +537,10 @@ struct Pages {
         id = x;
         kc = a.cache.k_scale[block] * (a.scale * 1.44269504088896340736f);
         vs = a.cache.v_scale[block];
-        if (vs < 0.0f) kc = __builtin_nanf("");  // (the weights of many rows take it as a logarithm)
+        // A scale that is negative, infinite or NaN: NaN through the scores, which the mask
+        // keeps from rows that do not see the page, and not through the values, whose zero
+        // weights there it would turn into NaN too.
+        if (!(vs >= 0.0f && vs < __builtin_inff())) kc = __builtin_nanf(""), vs = 1.0f;
       }
     }
   }

@@ -133,9 +133,9 @@ QPN_API size_t qpn_kv_attention_scratch_bytes(int requests, int max_rows, int q_
  * q: [rows, q_heads * dim] FP16 (row stride q_stride, a multiple of 8), y the
  * same (row stride y_stride, a multiple of 4).  A row that sees no token gives
  * zeros; what stands in tokens a row does not see (NaN included) never reaches
- * it.  A page number outside the cache, or a page whose values have a negative
- * scale, gives NaN in the rows that see it, and seq_lens[r] > 64 * table_width
- * gives NaN in all rows of r.  Requests whose
+ * it.  A page number outside the cache, or a page whose values' scale is
+ * negative, infinite or NaN, gives NaN in the rows that see it, and
+ * seq_lens[r] > 64 * table_width gives NaN in all rows of r.  Requests whose
  * row_start is out of order or past `rows` are skipped; rows of no request are
  * not written.  max_rows: the most rows of one request, a hint that the tile
  * is chosen by.

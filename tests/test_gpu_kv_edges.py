@@ -56,6 +56,26 @@ def test_attention_windows_of_rows_before_the_first_token(kv, dim, lens):
         assert np.array_equal(c.run(window=window), clean), window
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows,tokens", [(8, 130), (70, 150)])
+@pytest.mark.parametrize("scale", [np.nan, np.inf, -np.inf, -2.0])
+def test_attention_bad_value_scale_reaches_only_rows_that_see_the_page(kv, dim, rows, tokens, scale):
+    c = AttnCase(kv, [(rows, tokens), (rows, 64)], 4, 2, dim, 55)
+    first, heads = tokens - rows, slice(2, 4)      # the first row's position; the query heads of KV head 1
+    good = c.scale.copy()
+    for window, page in ((0, 2), (3, 1), (0, 1)):
+        clean = c.run(window=window)
+        c.scale[1, c.table[0, page], 1] = scale
+        y = c.run(window=window)
+        c.scale = good.copy()
+        hit = np.zeros(y.shape, bool)
+        for i in range(rows):
+            low = max(0, first + i + 1 - window) if window else 0
+            hit[i, heads] = first + i >= PAGE * page and low < PAGE * (page + 1)
+        assert hit.any() and np.array_equal(np.isnan(y), hit), (window, page)
+        c.check(np.where(hit, clean, y), window)
+
+
 # ---------------------------------------------------------------- rope_append
 
 def halfway_values(scale):
