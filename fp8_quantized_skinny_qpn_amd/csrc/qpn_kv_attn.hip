@@ -40,9 +40,14 @@ namespace {
 
 constexpr int kRsrc = 0x00020000;
 
-constexpr float kMaxSlack = 8.0f;     // how far (log2) a score may pass the running maximum
-constexpr float kScaleSlack = 64.0f;  // and a page's V scale the running one
-constexpr float kScaleLeast = 0x1p-20f;
+constexpr float kMaxSlack = 8.0f;       // how far (log2) a score may pass the running maximum
+// Many rows: the FP16 weights carry the page's V scale as a factor vs / vref, which stays
+// from 1 on (a smaller one would push weights among FP16's subnormal numbers and cost them
+// bits) to this (with the 2^8 above, weights stay below 2^15).  When a page leaves that
+// range vref, a power of two, is set anew: to the page's scale's less kScaleBelow.
+constexpr float kScaleSlack = 128.0f;
+constexpr int kScaleBelow = 3;          // (log2)
+constexpr float kScaleLeast = 0x1p-40f; // values of a smaller scale (they are below 2^-31) count as zeros
 constexpr float kLowest = -3e38f;     // the running maximum before any score
 
 // wavefronts of a workgroup, few rows: one per 16 dimensions up to eight
@@ -319,10 +324,15 @@ struct Rows {
   static constexpr int DT = DIM / 16;  // tiles of output dimensions
   float m[RT], sum[RT];
   float4v o[DT][RT];
-  float vref;  // what the sums are in units of
+  float vref;  // what the sums are in units of: a power of two
+
+  // The unit for a page scale of kScaleLeast or more.
+  static __device__ __forceinline__ float unit_for(float vs) {
+    return __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, vs) & 0x7F800000u) - ((uint32_t)kScaleBelow << 23));
+  }
 
   __device__ __forceinline__ void begin(float first_scale) {
-    vref = first_scale > 0x1p-100f ? first_scale : 0x1p-100f;
+    vref = unit_for(fmaxf(first_scale, kScaleLeast));
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       m[t] = kLowest;
@@ -332,20 +342,23 @@ struct Rows {
     }
   }
 
-  // Takes a page's V scale to one that is positive and in proportion to vref
-  // (uniform); false when the values count for nothing beside the others.
+  // Puts the sums into a unit that a page's V scale (finite, not negative; uniform)
+  // is in proportion to.  False when the page's values count as zeros: vs is then
+  // a scale in proportion.
   __device__ __forceinline__ bool settle(float& vs) {
-    if (vs > vref * kScaleSlack || (vs < vref * kScaleLeast && vs > vref * 0x1p-90f)) {
-      const float f = vref / vs;
-      vref = vs;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-        for (int d = 0; d < DT; ++d) o[d][rt] *= f;
-    } else if (vs <= vref * kScaleLeast) {
+    if (vs < kScaleLeast) {
       vs = vref;
       return false;
     }
+    const float to = unit_for(vs);
+    const int up = (int)(__builtin_bit_cast(uint32_t, vref) >> 23) - (int)(__builtin_bit_cast(uint32_t, to) >> 23);
+    vref = to;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) o[d][rt][r] = __builtin_amdgcn_ldexpf(o[d][rt][r], up);  // (exact)
     return true;
   }
 
@@ -392,7 +405,7 @@ struct Rows {
   }
 
   // The weights of a page's scores s, as the B operands of the second product
-  // (p[h]: tokens of tiles 2 h and 2 h + 1), times vs / vref:
+  // (p[h]: tokens of tiles 2 h and 2 h + 1), times vs / vref, 1 to kScaleSlack:
   // exp2(score - m + lift), lift = log2(vs / vref), with their FP32 sum times
   // vref / vs (drop) added to the sums; and the scores of the next page.  The
   // two in turn, operand by operand, so that the vector and the matrix unit
@@ -1211,7 +1224,7 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention_many_kernel(Attenti
         float vs = Pages::at(now.vs, at & 63);
         const int base = page * kKvPage;
         bool counts = true;
-        if (__builtin_expect(!(vs <= rows.vref * kScaleSlack && vs >= rows.vref * kScaleLeast), 0)) counts = rows.settle(vs);
+        if (__builtin_expect(!(vs >= rows.vref && vs <= rows.vref * kScaleSlack), 0)) counts = rows.settle(vs);
         if (base + kKvPage > see.lim_min || base < see.low_max) {
           mask_page<RT>(s, base, g, see);
 #pragma unroll

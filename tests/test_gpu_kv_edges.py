@@ -76,6 +76,54 @@ def test_attention_bad_value_scale_reaches_only_rows_that_see_the_page(kv, dim, 
         c.check(np.where(hit, clean, y), window)
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows,hq", [(2, 2), (64, 2), (60, 1)])
+@pytest.mark.parametrize("tokens", [64 * 6, 64 * 40])
+@pytest.mark.parametrize("ratio", [4, 8, 13, 16, 19, 24])
+def test_attention_weights_on_a_page_of_small_scale(kv, dim, rows, hq, tokens, ratio):
+    # All weight lies on page 3, whose values have a scale 2^ratio below the others'.  An output then is
+    # as exact as with equal scales: FP16 weights are off by 2^-11 of each, or 2^-25 of the row's largest
+    # below 2^-14 of it (and by no more than a weight itself), whatever the scales of other pages.
+    c = AttnCase(kv, [(rows, tokens)], hq, 1, dim, 56 + ratio)
+    page = c.table[0, 3]
+    c.codes[0] = 0xB8                              # keys: -1
+    c.codes[0, page] = 0x38                        # and 1 on the page, but for the first dimension: -1 .. 1
+    c.codes[0, page, :, :, 0] = np.random.default_rng(57).integers(0, 0x39, PAGE) | (np.arange(PAGE) % 2 * 0x80)
+    c.scale[0] = 1.0
+    c.scale[1] = 2.0 ** 10
+    c.scale[1, page] = 2.0 ** (10 - ratio)
+    c.q[:] = 20 / dim ** 0.5                       # scores +-20 by the page, +-6 within it
+    c.q[:, :, 0] = 6 * dim ** 0.5
+    y = c.run()
+    k, v = c.values()
+    ref, mag = kv_ref.attention(c.q.astype(np.float64), k, v, c.row_start, c.seq, np.clip(c.table, 0, None), dim ** -0.5, 0)
+    ids = c.table[0, :tokens // PAGE]
+    kk, vv = k[ids, 0].reshape(-1, dim), np.abs(v[ids, 0].reshape(-1, dim))
+    s = kk @ c.q[0, 0].astype(np.float64) * dim ** -0.5          # (all rows ask the same)
+    assert np.ptp(s) > 35 and s.argmax() // PAGE == 3
+    small = np.minimum(2.0 ** -25, np.exp(s - s.max())) @ vv
+    tol = 2.0 ** -11 * np.abs(ref) + (2.0 ** -11 + 2.0 ** -24 * (40 * dim + tokens)) * mag + small + 2.0 ** -25
+    err = np.abs(y - ref)
+    assert (err <= tol).all(), f"max error {(err / tol).max():.2f} of what is allowed, {(err > tol).sum()} outside"
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("rows", [4, 64])
+def test_attention_value_scales_over_the_whole_range(kv, dim, rows):
+    # page scales from what a page of zeros has to what FP16 cannot hold any more, in rising, falling and mixed order
+    c = AttnCase(kv, [(rows, 64 * 9 + 5)], 2, 1, dim, 58)
+    for powers in (np.linspace(-60, 9, 10), np.linspace(9, -60, 10), np.array([-60, 9, -30, 0, 9, -60, 4, -20, 1, -45])):
+        c.scale[1][c.table[0, :10], 0] = 2.0 ** np.round(powers)
+        c.check(c.run())
+    c.scale[1][c.table[0, :10], 0] = 2.0 ** np.array([-60, 100, -60, 0, 100, -100, 4, -149, 1, -45])
+    y = c.run()
+    ref, mag = kv_ref.attention(c.q.astype(np.float64), *c.values(), c.row_start, c.seq, np.clip(c.table, 0, None), dim ** -0.5, 0)
+    far = np.abs(ref) > 1e6 + 2.0 ** -10 * mag     # beyond FP16, and of a sign that rounded weights cannot change
+    assert far.mean() > 0.9 and (mag > 1e20).all() and np.isinf(y).all()
+    wrong = far & (y != np.copysign(np.inf, ref))
+    assert not wrong.any(), f"{wrong.sum()} signs, up to {(np.abs(ref) / mag)[wrong].max():.2e} of the magnitude"
+
+
 # ---------------------------------------------------------------- rope_append
 
 def halfway_values(scale):
