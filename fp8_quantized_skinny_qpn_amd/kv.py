@@ -127,23 +127,33 @@ class KvCache:
 
     k: float8_e4m3fn [pages, heads, dim / 16, 64, 16]: dimension 16 c + e of token t at [c, t, e];
     v: float8_e4m3fn [pages, heads, dim, 64]: dimension d of token 16 t + 4 g + r at
-    [d, 16 g + 4 t + r]; k_scale, v_scale: float32 [pages, heads]."""
+    [d, 16 g + 4 t + r]; k_scale, v_scale: float32 [pages, heads].  Setting a field (a cache that
+    grows) takes effect at the next call, which checks them all."""
 
     def __init__(self, k, v, k_scale, v_scale):
-        if k.dim() != 5 or k.shape[3] != PAGE or k.shape[4] != 16:
-            raise ValueError("keys must be [pages, heads, dim / 16, 64, 16]")
-        pages, heads, dim = k.shape[0], k.shape[1], k.shape[2] * 16
-        if tuple(v.shape) != (pages, heads, dim, PAGE):
-            raise ValueError("values must be [pages, heads, dim, 64]")
-        if tuple(k_scale.shape) != (pages, heads) or tuple(v_scale.shape) != (pages, heads):
-            raise ValueError("scales must be [pages, heads]")
-        f8 = torch.float8_e4m3fn
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self.pages, self.heads, self.dim = pages, heads, dim
-        self._c = _Cache(_need(k, f8, 5, "keys"), _need(v, f8, 4, "values"),
-                         _need(k_scale, torch.float32, 2, "key scales"),
-                         _need(v_scale, torch.float32, 2, "value scales"), pages, heads, dim)
-        self._ref = ctypes.byref(self._c)
+        self._checked()
+
+    def __setattr__(self, name, value):
+        if name == "k":
+            if value.dim() != 5 or value.shape[3] != PAGE or value.shape[4] != 16:
+                raise ValueError("keys must be [pages, heads, dim / 16, 64, 16]")
+            self.__dict__.update(pages=value.shape[0], heads=value.shape[1], dim=value.shape[2] * 16)
+        self.__dict__["_ref"] = None
+        self.__dict__[name] = value
+
+    def _checked(self):
+        """The C struct of the tensors, checked once after a field is set."""
+        if self._ref is None:
+            pages, heads, dim, f8, f32 = self.pages, self.heads, self.dim, torch.float8_e4m3fn, torch.float32
+            if tuple(self.v.shape) != (pages, heads, dim, PAGE):
+                raise ValueError("values must be [pages, heads, dim, 64]")
+            if tuple(self.k_scale.shape) != (pages, heads) or tuple(self.v_scale.shape) != (pages, heads):
+                raise ValueError("scales must be [pages, heads]")
+            self.__dict__["_ref"] = ctypes.byref(_Cache(
+                _need(self.k, f8, 5, "keys"), _need(self.v, f8, 4, "values"), _need(self.k_scale, f32, 2, "key scales"),
+                _need(self.v_scale, f32, 2, "value scales"), pages, heads, dim))
+        return self._ref
 
     @classmethod
     def empty(cls, pages: int, heads: int, dim: int, device="cuda") -> "KvCache":
@@ -231,7 +241,7 @@ def rope_append(cache: KvCache, qkv, q_heads: int, positions, slots, inv_freq, q
         raise ValueError(f"out must be [{rows}, {q_heads * d}]")
     f16, i32 = torch.float16, torch.int32
     check(lib.qpn_kv_rope_append(
-        cache._ref, qp, qs, rows, q_heads, None if q_weight is None else _need(q_weight, f16, 1, "q_weight"),
+        cache._checked(), qp, qs, rows, q_heads, None if q_weight is None else _need(q_weight, f16, 1, "q_weight"),
         None if k_weight is None else _need(k_weight, f16, 1, "k_weight"), eps,
         None if inv_freq is None else _need(inv_freq, torch.float32, 1, "inv_freq"),
         0 if inv_freq is None else 2 * inv_freq.shape[0], interleaved, _need(positions, i32, 1, "positions"),
@@ -267,7 +277,7 @@ def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scal
         need = attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
         scratch_ = _scratch(need if need < 1 << 63 else 0, q.device, raw, stream)
     check(lib.qpn_kv_attention(
-        cache._ref, qp, qs, yp, ys, heads, q.shape[0], n, max_rows, _need(row_start, torch.int32, 1, "row_start"),
+        cache._checked(), qp, qs, yp, ys, heads, q.shape[0], n, max_rows, _need(row_start, torch.int32, 1, "row_start"),
         _need(seq_lens, torch.int32, 1, "seq_lens"), tp, tstride, width, d ** -0.5 if scale is None else scale,
         window, scratch_.data_ptr(), scratch_.numel(), raw))
     return out
