@@ -15,6 +15,8 @@ One round, on the device throughout::
     accepted, token, prob = kv.verify_sampled(logits, tokens, r.row_start, accept_u, sample_u)
 """
 import ctypes
+import threading
+from contextlib import nullcontext
 from dataclasses import dataclass
 from functools import lru_cache
 
@@ -96,8 +98,21 @@ def _raw_stream(stream) -> int:
 # head is left zero by every call, the rest holds anything.  Allocated and
 # zeroed on the stream that uses it.  A buffer that grows is kept next to its
 # successor (at least twice its size), since a captured graph may hold it.
+# A call of several launches passes its sums on through the scratch, so a call
+# holds its scratch's lock until all of them are queued: threads that share a
+# stream queue whole calls one after another.
 _scratches = {}
 _outgrown = []
+_locks = {}
+_unlocked = nullcontext()
+
+
+def _lock_of(given, device, raw: int):
+    """What a call holds: the lock of the stream's scratch, or nothing when it is given one."""
+    if given is not None:
+        return _unlocked
+    key = (device.index, raw)
+    return _locks.get(key) or _locks.setdefault(key, threading.Lock())
 
 
 def scratch(nbytes: int, device, stream) -> torch.Tensor:
@@ -273,13 +288,14 @@ def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scal
     elif out.shape != q.shape:
         raise ValueError("out must have the queries' shape")
     yp, ys = _rows(out, "out")
-    if scratch_ is None:
-        need = attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
-        scratch_ = _scratch(need if need < 1 << 63 else 0, q.device, raw, stream)
-    check(lib.qpn_kv_attention(
-        cache._checked(), qp, qs, yp, ys, heads, q.shape[0], n, max_rows, _need(row_start, torch.int32, 1, "row_start"),
-        _need(seq_lens, torch.int32, 1, "seq_lens"), tp, tstride, width, d ** -0.5 if scale is None else scale,
-        window, scratch_.data_ptr(), scratch_.numel(), raw))
+    with _lock_of(scratch_, q.device, raw):
+        if scratch_ is None:
+            need = attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
+            scratch_ = _scratch(need if need < 1 << 63 else 0, q.device, raw, stream)
+        check(lib.qpn_kv_attention(
+            cache._checked(), qp, qs, yp, ys, heads, q.shape[0], n, max_rows,
+            _need(row_start, torch.int32, 1, "row_start"), _need(seq_lens, torch.int32, 1, "seq_lens"), tp, tstride,
+            width, d ** -0.5 if scale is None else scale, window, scratch_.data_ptr(), scratch_.numel(), raw))
     return out
 
 
@@ -312,12 +328,13 @@ def verify_sampled(logits, tokens, row_start, accept_u, sample_u, draft_logits=N
     accepted, token, prob = out
     if accepted.shape[0] != requests or token.shape[0] != requests or prob.shape[0] != rows:
         raise ValueError("out must be (accepted [requests], next [requests], accept_prob [rows])")
-    if scratch_ is None:
-        need = verify_scratch_bytes(rows, requests, n)
-        scratch_ = _scratch(need if need < 1 << 63 else 0, dev, raw, stream)
-    check(lib.qpn_kv_verify_sampled(
-        lp, ls, dp or None, ds, _need(tokens, i32, 1, "tokens"), _need(row_start, i32, 1, "row_start"), rows,
-        requests, n, 1.0 / temperature, _need(accept_u, f32, 1, "accept_u"), _need(sample_u, f32, 1, "sample_u"),
-        _need(accepted, i32, 1, "accepted"), _need(token, i32, 1, "next"), _need(prob, f32, 1, "accept_prob"),
-        scratch_.data_ptr(), scratch_.numel(), raw))
+    with _lock_of(scratch_, dev, raw):
+        if scratch_ is None:
+            need = verify_scratch_bytes(rows, requests, n)
+            scratch_ = _scratch(need if need < 1 << 63 else 0, dev, raw, stream)
+        check(lib.qpn_kv_verify_sampled(
+            lp, ls, dp or None, ds, _need(tokens, i32, 1, "tokens"), _need(row_start, i32, 1, "row_start"), rows,
+            requests, n, 1.0 / temperature, _need(accept_u, f32, 1, "accept_u"),
+            _need(sample_u, f32, 1, "sample_u"), _need(accepted, i32, 1, "accepted"), _need(token, i32, 1, "next"),
+            _need(prob, f32, 1, "accept_prob"), scratch_.data_ptr(), scratch_.numel(), raw))
     return out

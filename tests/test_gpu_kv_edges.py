@@ -2,12 +2,16 @@
 
 References and tolerances are those of test_gpu_kv.py; where one differs it is derived at its test.
 """
+import threading
+import time
+
 import numpy as np
 import pytest
+import torch
 
 import kv_ref
-from gpu_util import need_gpu
-from test_gpu_kv import PAGE, AttnCase, append_case, run_slots
+from gpu_util import dev, need_gpu
+from test_gpu_kv import PAGE, AttnCase, append_case, i32, run_slots, verify_case
 
 pytestmark = pytest.mark.gpu
 
@@ -151,3 +155,65 @@ def test_append_odd_scales_of_rotated_keys(kv):
     slots, pos = run_slots([(1000, 300), (70, 30), (63, 66)], 14, 52)
     for old in (0.0123, 0.7, 37.3):
         append_case(kv, 128, 4, 2, slots, pos, 14, 53, old=old)
+
+
+# ---------------------------------------------------------------- scratch
+
+class Watched:
+    """Stands before the library: notes the scratch of each call, and calls that have one at the same time."""
+
+    def __init__(self, lib, launch):
+        self.lib, self.launch, self.given, self.inside, self.clashes = lib, launch, [], [], 0
+
+    def __getattr__(self, name):
+        f = getattr(self.lib, name)
+        if name not in ("qpn_kv_attention", "qpn_kv_verify_sampled"):
+            return f
+
+        def call(*args):
+            scratch = args[-3]                     # .., scratch, its bytes, stream
+            self.given.append(scratch)
+            if self.launch:
+                return f(*args)
+            self.clashes += scratch in self.inside
+            self.inside.append(scratch)
+            time.sleep(0.002)                      # (another thread may run)
+            self.inside.remove(scratch)
+            return 0
+        return call
+
+
+def attention_call(kv, seed=60, tokens=3000):
+    """A call whose pieces meet in the scratch: (call(stream, out), its outputs' bits)."""
+    c = AttnCase(kv, [(8, tokens)], 10, 2, 128, seed)
+    q, row_start, seq, table, cache = dev(c.q.reshape(8, -1)), i32(c.row_start), i32(c.seq), i32(c.table), c.device()
+    return (lambda stream=None, out=None: kv.attention(cache, q, row_start, seq, table, 8, stream=stream, out=out),
+            c.run().reshape(8, -1))
+
+
+def test_threads_do_not_share_a_scratch_at_the_same_time(kv, monkeypatch):
+    # a call of two launches hands its sums over through the scratch: on one stream, the launches of two
+    # threads' calls must not come in turn
+    call, _ = attention_call(kv)
+    _, _, args = verify_case(kv, [4, 4], 5000, 61, True)
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    call(stream), kv.verify_sampled(*args, stream=stream)
+    torch.cuda.synchronize()
+    watch = Watched(kv.lib, launch=False)
+    monkeypatch.setattr(kv, "lib", watch)
+    failed = []
+
+    def work(f):
+        try:
+            for _ in range(10):
+                f()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(f,)) for f in (
+        lambda: call(stream), lambda: kv.verify_sampled(*args, stream=stream), lambda: call(stream))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed and len(watch.given) == 30 and watch.clashes == 0
