@@ -96,44 +96,61 @@ def _raw_stream(stream) -> int:
 
 # Scratch of attention and verification, one per (device, stream): its zeroed
 # head is left zero by every call, the rest holds anything.  Allocated and
-# zeroed on the stream that uses it.  A buffer that grows is kept next to its
-# successor (at least twice its size), since a captured graph may hold it.
+# zeroed on the stream that uses it, so that a buffer which grows can be let go.
 # A call of several launches passes its sums on through the scratch, so a call
 # holds its scratch's lock until all of them are queued: threads that share a
-# stream queue whole calls one after another.
+# stream queue whole calls one after another.  Calls under capture take a scratch
+# of the capture's own: the graph may be replayed on any stream, beside other
+# graphs and calls.  It is allocated in the graph's memory and zeroed by a node of
+# the graph, once for all of its calls on that stream.
 _scratches = {}
-_outgrown = []
-_locks = {}
-_unlocked = nullcontext()
+_captured = {}             # (device, stream): (number of its last capture, scratch)
+_unlocked = nullcontext()  # for a call that is given its scratch
 
 
-def _lock_of(given, device, raw: int):
-    """What a call holds: the lock of the stream's scratch, or nothing when it is given one."""
-    if given is not None:
-        return _unlocked
-    key = (device.index, raw)
-    return _locks.get(key) or _locks.setdefault(key, threading.Lock())
+class _Locks(dict):
+    def __missing__(self, key):
+        return self.setdefault(key, threading.Lock())
+
+
+_locks = _Locks()
+
+
+def _capture_of(raw: int, stream) -> int:
+    """The number of the capture that the stream is in, 0 for none."""
+    if stream is None and not torch._C._cuda_isCurrentStreamCapturing():
+        return 0
+    status, number = ctypes.c_int(), ctypes.c_ulonglong()  # (asked of the HIP runtime that the library is linked with)
+    if lib.hipStreamGetCaptureInfo(ctypes.c_void_p(raw), ctypes.byref(status), ctypes.byref(number)):
+        return 0
+    return number.value if status.value == 1 else 0
 
 
 def scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """The cached scratch of at least nbytes for `stream` (a torch stream) on `device`."""
-    return _scratch(nbytes, device, stream.cuda_stream, stream)
+    """The scratch of at least nbytes for `stream` (a torch stream) on `device`."""
+    key = (torch.device(device).index, stream.cuda_stream)
+    with _locks[key]:
+        return _scratch(nbytes, key, stream)
 
 
-def _scratch(nbytes: int, device, raw: int, stream) -> torch.Tensor:
-    key = (device.index, raw)
-    s = _scratches.get(key)
+def _scratch(nbytes: int, key, stream) -> torch.Tensor:
+    """The scratch of at least nbytes for a call on a stream (whose lock the caller holds)."""
+    raw = key[1]
+    capture = raw and _capture_of(raw, stream)  # (the null stream is never captured)
+    if capture:
+        number, s = _captured.get(key, (0, None))
+        s = s if number == capture else None
+    else:
+        s = _scratches.get(key)
     if s is None or s.numel() < nbytes:
-        stream = _torch_stream(stream)
         nbytes = max(nbytes, SCRATCH_ZEROED, 0 if s is None else 2 * s.numel())
-        with torch.cuda.stream(stream):
-            new = torch.empty(nbytes, dtype=torch.uint8, device=device)
-            new[:SCRATCH_ZEROED].zero_()
-            if torch.cuda.is_current_stream_capturing():
-                return new  # the graph's own: it is zeroed when the graph runs, not now
-        if s is not None:
-            _outgrown.append(s)
-        _scratches[key] = s = new
+        with torch.cuda.stream(_torch_stream(stream)):
+            s = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", key[0]))
+            s[:SCRATCH_ZEROED].zero_()
+        if capture:
+            _captured[key] = (capture, s)
+        else:
+            _scratches[key] = s
     return s
 
 
@@ -288,10 +305,11 @@ def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scal
     elif out.shape != q.shape:
         raise ValueError("out must have the queries' shape")
     yp, ys = _rows(out, "out")
-    with _lock_of(scratch_, q.device, raw):
+    key = (q.get_device(), raw)
+    with _locks[key] if scratch_ is None else _unlocked:
         if scratch_ is None:
             need = attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
-            scratch_ = _scratch(need if need < 1 << 63 else 0, q.device, raw, stream)
+            scratch_ = _scratch(need if need < 1 << 63 else 0, key, stream)
         check(lib.qpn_kv_attention(
             cache._checked(), qp, qs, yp, ys, heads, q.shape[0], n, max_rows,
             _need(row_start, torch.int32, 1, "row_start"), _need(seq_lens, torch.int32, 1, "seq_lens"), tp, tstride,
@@ -328,10 +346,11 @@ def verify_sampled(logits, tokens, row_start, accept_u, sample_u, draft_logits=N
     accepted, token, prob = out
     if accepted.shape[0] != requests or token.shape[0] != requests or prob.shape[0] != rows:
         raise ValueError("out must be (accepted [requests], next [requests], accept_prob [rows])")
-    with _lock_of(scratch_, dev, raw):
+    key = (logits.get_device(), raw)
+    with _locks[key] if scratch_ is None else _unlocked:
         if scratch_ is None:
             need = verify_scratch_bytes(rows, requests, n)
-            scratch_ = _scratch(need if need < 1 << 63 else 0, dev, raw, stream)
+            scratch_ = _scratch(need if need < 1 << 63 else 0, key, stream)
         check(lib.qpn_kv_verify_sampled(
             lp, ls, dp or None, ds, _need(tokens, i32, 1, "tokens"), _need(row_start, i32, 1, "row_start"), rows,
             requests, n, 1.0 / temperature, _need(accept_u, f32, 1, "accept_u"),

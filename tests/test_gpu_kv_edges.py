@@ -10,7 +10,7 @@ import pytest
 import torch
 
 import kv_ref
-from gpu_util import dev, need_gpu
+from gpu_util import dev, host, need_gpu
 from test_gpu_kv import PAGE, AttnCase, append_case, i32, run_slots, verify_case
 
 pytestmark = pytest.mark.gpu
@@ -217,3 +217,61 @@ def test_threads_do_not_share_a_scratch_at_the_same_time(kv, monkeypatch):
     for t in threads:
         t.join()
     assert not failed and len(watch.given) == 30 and watch.clashes == 0
+
+
+def test_graphs_of_a_stream_have_scratch_of_their_own(kv, monkeypatch):
+    # the stream has a scratch already; graphs captured on it may run beside each other and beside its calls
+    calls = [attention_call(kv, 62), attention_call(kv, 63, 6000)]
+    stream, others = torch.cuda.Stream(), [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for call, want in calls:
+        assert np.array_equal(host(call(stream)), want)
+    watch = Watched(kv.lib, launch=True)
+    monkeypatch.setattr(kv, "lib", watch)
+    held = {s.data_ptr() for s in kv._scratches.values()}
+    graphs, outs = [], []
+    for call, want in calls:
+        g, out = torch.cuda.CUDAGraph(), [torch.zeros(want.shape, dtype=torch.float16, device="cuda") for _ in range(3)]
+        torch.cuda.synchronize()
+        before = len(watch.given)
+        with torch.cuda.graph(g, stream=stream):
+            for o in out:
+                call(out=o)
+        mine = set(watch.given[before:])
+        assert len(mine) == 1 and not mine & held  # one for the graph's calls, and nobody else's
+        held |= mine
+        graphs.append(g)
+        outs.append(out)
+    for _ in range(4):
+        for out in outs:
+            for o in out:
+                o.zero_()
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, others):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = [calls[0][0](stream) for _ in range(3)]
+        torch.cuda.synchronize()
+        for o in eager:
+            assert np.array_equal(host(o), calls[0][1])
+        for out, (_, want) in zip(outs, calls):
+            for o in out:
+                assert np.array_equal(host(o), want)
+
+
+def test_scratch_that_grows_within_a_capture(kv):
+    calls = [attention_call(kv, 64, 700), attention_call(kv, 65, 6000)]
+    stream, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    outs = [torch.zeros(8, 1280, dtype=torch.float16, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=stream):
+        for i, o in enumerate(outs):
+            calls[i % 2][0](out=o)
+    for _ in range(3):
+        for o in outs:
+            o.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        for i, o in enumerate(outs):
+            assert np.array_equal(host(o), calls[i % 2][1])
+        assert np.array_equal(host(calls[0][0]()), calls[0][1])

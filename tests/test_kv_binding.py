@@ -57,3 +57,7 @@ def test_cache_follows_its_fields(kv, monkeypatch):
     c.k, c.v, c.k_scale, c.v_scale = wide.k, wide.v, wide.k_scale, wide.v_scale
     s = struct_of(kv, c)
     assert (s.pages, s.heads, s.dim) == (c.pages, c.heads, c.dim) == (4, 3, 256)
+
+
+def test_capture_is_asked_of_the_runtime(kv):
+    assert kv.lib.hipStreamGetCaptureInfo            # (of the HIP runtime that the library is linked with)
