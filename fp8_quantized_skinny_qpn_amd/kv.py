@@ -15,14 +15,13 @@ One round, on the device throughout::
     accepted, token, prob = kv.verify_sampled(logits, tokens, r.row_start, accept_u, sample_u)
 """
 import ctypes
-import threading
 from contextlib import nullcontext
 from dataclasses import dataclass
 from functools import lru_cache
 
 import torch
 
-from .qpn import LIB_PATH, QpnError, _empty, _torch_stream, check, lib  # noqa: F401
+from .qpn import LIB_PATH, QpnError, StreamBuffers, _empty, _torch_stream, check, lib  # noqa: F401
 
 PAGE = 64
 SCRATCH_ZEROED = 65536
@@ -94,64 +93,18 @@ def _raw_stream(stream) -> int:
     return stream.cuda_stream
 
 
-# Scratch of attention and verification, one per (device, stream): its zeroed
-# head is left zero by every call, the rest holds anything.  Allocated and
-# zeroed on the stream that uses it, so that a buffer which grows can be let go.
-# A call of several launches passes its sums on through the scratch, so a call
-# holds its scratch's lock until all of them are queued: threads that share a
-# stream queue whole calls one after another.  Calls under capture take a scratch
-# of the capture's own: the graph may be replayed on any stream, beside other
-# graphs and calls.  It is allocated in the graph's memory and zeroed by a node of
-# the graph, once for all of its calls on that stream.
-_scratches = {}
-_captured = {}             # (device, stream): (number of its last capture, scratch)
+# Scratch of attention and verification: its zeroed head is left zero by every
+# call, the rest holds anything.  A call of several launches passes its sums on
+# through the scratch, so a call holds its scratch's lock until all of them are
+# queued: threads that share a stream queue whole calls one after another.
+_buffers = StreamBuffers(SCRATCH_ZEROED, SCRATCH_ZEROED)
+_scratches, _locks = _buffers.held, _buffers.locks
 _unlocked = nullcontext()  # for a call that is given its scratch
-
-
-class _Locks(dict):
-    def __missing__(self, key):
-        return self.setdefault(key, threading.Lock())
-
-
-_locks = _Locks()
-
-
-def _capture_of(raw: int, stream) -> int:
-    """The number of the capture that the stream is in, 0 for none."""
-    if stream is None and not torch._C._cuda_isCurrentStreamCapturing():
-        return 0
-    status, number = ctypes.c_int(), ctypes.c_ulonglong()  # (asked of the HIP runtime that the library is linked with)
-    if lib.hipStreamGetCaptureInfo(ctypes.c_void_p(raw), ctypes.byref(status), ctypes.byref(number)):
-        return 0
-    return number.value if status.value == 1 else 0
 
 
 def scratch(nbytes: int, device, stream) -> torch.Tensor:
     """The scratch of at least nbytes for `stream` (a torch stream) on `device`."""
-    key = (torch.device(device).index, stream.cuda_stream)
-    with _locks[key]:
-        return _scratch(nbytes, key, stream)
-
-
-def _scratch(nbytes: int, key, stream) -> torch.Tensor:
-    """The scratch of at least nbytes for a call on a stream (whose lock the caller holds)."""
-    raw = key[1]
-    capture = raw and _capture_of(raw, stream)  # (the null stream is never captured)
-    if capture:
-        number, s = _captured.get(key, (0, None))
-        s = s if number == capture else None
-    else:
-        s = _scratches.get(key)
-    if s is None or s.numel() < nbytes:
-        nbytes = max(nbytes, SCRATCH_ZEROED, 0 if s is None else 2 * s.numel())
-        with torch.cuda.stream(_torch_stream(stream)):
-            s = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", key[0]))
-            s[:SCRATCH_ZEROED].zero_()
-        if capture:
-            _captured[key] = (capture, s)
-        else:
-            _scratches[key] = s
-    return s
+    return _buffers.get(nbytes, (torch.device(device).index, stream.cuda_stream), stream)
 
 
 class KvCache:
@@ -273,7 +226,7 @@ def rope_append(cache: KvCache, qkv, q_heads: int, positions, slots, inv_freq, q
         raise ValueError(f"out must be [{rows}, {q_heads * d}]")
     f16, i32 = torch.float16, torch.int32
     check(lib.qpn_kv_rope_append(
-        cache._checked(), qp, qs, rows, q_heads, None if q_weight is None else _need(q_weight, f16, 1, "q_weight"),
+        cache._ref or cache._checked(), qp, qs, rows, q_heads, None if q_weight is None else _need(q_weight, f16, 1, "q_weight"),
         None if k_weight is None else _need(k_weight, f16, 1, "k_weight"), eps,
         None if inv_freq is None else _need(inv_freq, torch.float32, 1, "inv_freq"),
         0 if inv_freq is None else 2 * inv_freq.shape[0], interleaved, _need(positions, i32, 1, "positions"),
@@ -292,26 +245,27 @@ def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scal
     `max_rows`: the most rows of one request (a hint).  `scale` defaults to dim ** -0.5."""
     d = cache.dim
     n = seq_lens.shape[0]
-    if q.dim() != 2 or q.shape[1] % d:
+    shape = q.shape
+    if len(shape) != 2 or shape[1] % d:
         raise ValueError(f"queries must be [rows, heads * {d}]")
     if row_start.shape[0] != n + 1:
         raise ValueError("row_start must have one entry more than seq_lens")
-    heads = q.shape[1] // d
+    heads = shape[1] // d
     qp, qs = _rows(q, "queries")
     tp, tstride, width = _table(table, n)
     raw = _raw_stream(stream)
     if out is None:
-        out = _empty(_torch_stream(stream), tuple(q.shape), torch.float16, q.device)
-    elif out.shape != q.shape:
+        out = _empty(_torch_stream(stream), tuple(shape), torch.float16, q.device)
+    elif out.shape != shape:
         raise ValueError("out must have the queries' shape")
     yp, ys = _rows(out, "out")
     key = (q.get_device(), raw)
     with _locks[key] if scratch_ is None else _unlocked:
         if scratch_ is None:
             need = attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
-            scratch_ = _scratch(need if need < 1 << 63 else 0, key, stream)
+            scratch_ = _buffers.get(need if need < 1 << 63 else 0, key, stream)
         check(lib.qpn_kv_attention(
-            cache._checked(), qp, qs, yp, ys, heads, q.shape[0], n, max_rows,
+            cache._ref or cache._checked(), qp, qs, yp, ys, heads, shape[0], n, max_rows,
             _need(row_start, torch.int32, 1, "row_start"), _need(seq_lens, torch.int32, 1, "seq_lens"), tp, tstride,
             width, d ** -0.5 if scale is None else scale, window, scratch_.data_ptr(), scratch_.numel(), raw))
     return out
@@ -350,7 +304,7 @@ def verify_sampled(logits, tokens, row_start, accept_u, sample_u, draft_logits=N
     with _locks[key] if scratch_ is None else _unlocked:
         if scratch_ is None:
             need = verify_scratch_bytes(rows, requests, n)
-            scratch_ = _scratch(need if need < 1 << 63 else 0, key, stream)
+            scratch_ = _buffers.get(need if need < 1 << 63 else 0, key, stream)
         check(lib.qpn_kv_verify_sampled(
             lp, ls, dp or None, ds, _need(tokens, i32, 1, "tokens"), _need(row_start, i32, 1, "row_start"), rows,
             requests, n, 1.0 / temperature, _need(accept_u, f32, 1, "accept_u"),

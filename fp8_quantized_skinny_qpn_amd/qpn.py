@@ -7,6 +7,7 @@ is no fallback of any kind.
 """
 import ctypes
 import os
+import threading
 from dataclasses import dataclass
 
 import torch
@@ -187,27 +188,70 @@ def kernel_name(fmt: str, m: int, n: int, k: int, lmhead: bool = False, plan: in
             f"{'true' if pl.valu_dot else 'false'}>")
 
 
-# Zero-initialised workspaces, one per (device, stream): the library leaves a
-# workspace's split-K counters at zero after every call, so a workspace is
-# zeroed once, when it is allocated, and then reused by calls on its stream.
-# It is allocated and zeroed on that stream, so the zero-fill is ordered
-# before every kernel that uses it, and a replaced buffer is kept alive
-# until the work already queued on the stream is done.
-_workspaces = {}
+def _capture_of(raw: int, stream) -> int:
+    """The number of the capture that a stream is in, 0 for none.  raw: the stream, not the null one (which
+    is in none); stream: its torch stream, or None for the current one."""
+    current = stream is None or raw == torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if current and not torch._C._cuda_isCurrentStreamCapturing():
+        return 0
+    status, number = ctypes.c_int(), ctypes.c_ulonglong()  # (asked of the HIP runtime that the library is linked with)
+    if lib.hipStreamGetCaptureInfo(ctypes.c_void_p(raw), ctypes.byref(status), ctypes.byref(number)):
+        return 0
+    return number.value if status.value == 1 else 0
+
+
+class _Locks(dict):
+    def __missing__(self, key):
+        return self.setdefault(key, threading.Lock())
+
+
+class StreamBuffers:
+    """Device buffers that calls share, one per (device, stream).
+
+    The first `zeroed` bytes of a buffer (None: all) are zero when it is made and are left zero by
+    every call, so it is zeroed once.  It is allocated and zeroed on its stream, so the zero-fill
+    is ordered before every kernel that uses it, and one that grows can be let go.
+
+    Calls under capture share a buffer of the capture's own, since the graph may be replayed on any
+    stream, beside other graphs and calls: it is allocated in the graph's memory and zeroed by a node
+    of the graph."""
+
+    def __init__(self, least: int, zeroed: int = None):
+        self.least, self.zeroed = least, zeroed
+        self.held = {}      # (device, stream): buffer
+        self.captured = {}  # (device, stream): (number of its last capture, buffer)
+        self.locks = _Locks()
+
+    def get(self, nbytes: int, key, stream=None) -> torch.Tensor:
+        """The buffer of at least nbytes of key = (device index, raw stream); `stream`: its torch stream
+        (None: the current one)."""
+        capture = key[1] and _capture_of(key[1], stream)
+        if capture:
+            number, b = self.captured.get(key, (0, None))
+            b = b if number == capture else None
+        else:
+            b = self.held.get(key)
+        if b is None or b.numel() < nbytes:
+            with torch.cuda.stream(_torch_stream(stream)):
+                b = torch.empty(max(nbytes, self.least), dtype=torch.uint8, device=torch.device("cuda", key[0]))
+                b[:self.zeroed].zero_()
+            if capture:
+                self.captured[key] = (capture, b)
+            else:
+                self.held[key] = b
+        return b
+
+
+# Zero-initialised workspaces: the library leaves a workspace's split-K counters
+# at zero after every call.
+_buffers = StreamBuffers(256)
+_workspaces = _buffers.held
 
 
 def workspace(nbytes: int, device, stream) -> torch.Tensor:
-    """The cached zero-filled workspace of at least nbytes for `stream` (a
-    torch stream) on `device`."""
-    key = (torch.device(device).index, stream.cuda_stream)
-    ws = _workspaces.get(key)
-    if ws is None or ws.numel() < nbytes:
-        with torch.cuda.stream(stream):
-            new = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
-        if ws is not None:
-            ws.record_stream(stream)
-        _workspaces[key] = ws = new
-    return ws
+    """The zero-filled workspace of at least nbytes that calls on `stream` (a
+    torch stream) of `device` share."""
+    return _buffers.get(nbytes, (torch.device(device).index, stream.cuda_stream), stream)
 
 
 @dataclass
