@@ -8,6 +8,7 @@ is no fallback of any kind.
 import ctypes
 import os
 import threading
+from contextlib import nullcontext
 from dataclasses import dataclass
 
 import torch
@@ -254,6 +255,13 @@ def workspace(nbytes: int, device, stream) -> torch.Tensor:
     return _buffers.get(nbytes, (torch.device(device).index, stream.cuda_stream), stream)
 
 
+def _whole_call(given, x, ts):
+    """What a call of two launches holds while it queues them: the lock of the stream's workspace (nothing
+    when it is given one), through which the first passes its results on.  Threads that share a stream
+    queue whole calls one after another."""
+    return _buffers.locks[x.get_device(), ts.cuda_stream] if given is None else nullcontext()
+
+
 @dataclass
 class PackedWeight:
     """A packed weight blob on the device plus the shape it was packed for."""
@@ -383,13 +391,14 @@ def lmhead_nvfp4(pw: PackedWeight, x: torch.Tensor, logits=None, argmax=None, wo
     if argmax is None:
         argmax = _empty(ts, (m,), torch.int32, x.device)
     need = workspace_bytes(OP_LMHEAD_NVFP4, m, pw.n, pw.k, plan)
-    ws = workspace_ if workspace_ is not None else workspace(max(need, 8), x.device, ts)
-    if plan == 0:
-        check(lib.qpn_lmhead_nvfp4(_ptr(pw.blob), _ptr(x), _ptr(logits), _ptr(argmax), m, pw.n,
-                                   pw.k, _ptr(ws), ws.numel(), st))
-    else:
-        check(lib.qpn_debug_run_plan(OP_LMHEAD_NVFP4, plan, _ptr(pw.blob), _ptr(x), _ptr(logits),
-                                     _ptr(argmax), m, pw.n, pw.k, _ptr(ws), ws.numel(), st))
+    with _whole_call(workspace_, x, ts):
+        ws = workspace_ if workspace_ is not None else workspace(max(need, 8), x.device, ts)
+        if plan == 0:
+            check(lib.qpn_lmhead_nvfp4(_ptr(pw.blob), _ptr(x), _ptr(logits), _ptr(argmax), m, pw.n,
+                                       pw.k, _ptr(ws), ws.numel(), st))
+        else:
+            check(lib.qpn_debug_run_plan(OP_LMHEAD_NVFP4, plan, _ptr(pw.blob), _ptr(x), _ptr(logits),
+                                         _ptr(argmax), m, pw.n, pw.k, _ptr(ws), ws.numel(), st))
     return logits, argmax
 
 
@@ -414,10 +423,11 @@ def lmhead_verify_nvfp4(pw: PackedWeight, x: torch.Tensor, draft: torch.Tensor, 
     if result is None:
         result = _empty(ts, (2,), torch.int32, x.device)
     need = workspace_bytes(OP_LMHEAD_NVFP4, m, pw.n, pw.k)
-    ws = workspace_ if workspace_ is not None else workspace(max(need, 8), x.device, ts)
-    check(lib.qpn_lmhead_verify_nvfp4(_ptr(pw.blob), _ptr(x), _ptr(logits), _ptr(argmax),
-                                      _ptr(draft) if draft.numel() else None, _ptr(result), m,
-                                      pw.n, pw.k, _ptr(ws), ws.numel(), st))
+    with _whole_call(workspace_, x, ts):
+        ws = workspace_ if workspace_ is not None else workspace(max(need, 8), x.device, ts)
+        check(lib.qpn_lmhead_verify_nvfp4(_ptr(pw.blob), _ptr(x), _ptr(logits), _ptr(argmax),
+                                          _ptr(draft) if draft.numel() else None, _ptr(result), m,
+                                          pw.n, pw.k, _ptr(ws), ws.numel(), st))
     return logits, argmax, result
 
 

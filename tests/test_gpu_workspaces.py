@@ -1,5 +1,8 @@
 """Workspaces that the products' calls share: a graph has its own, so it may be captured and replayed beside
 eager calls and other graphs.  Results are compared bit for bit with those of eager calls."""
+import threading
+import time
+
 import numpy as np
 import pytest
 import torch
@@ -11,19 +14,27 @@ pytestmark = pytest.mark.gpu
 
 
 class Given:
-    """Stands before the library and notes the workspace of each call."""
+    """Stands before the library and notes the workspace of each call; without `launch` nothing is
+    launched, and calls that have a workspace at the same time are counted."""
 
-    def __init__(self, lib):
-        self.lib, self.given = lib, []
+    def __init__(self, lib, launch=True):
+        self.lib, self.launch, self.given, self.inside, self.clashes = lib, launch, [], [], 0
 
     def __getattr__(self, name):
         f = getattr(self.lib, name)
-        if name not in ("qpn_gemm_nvfp4", "qpn_gemm_prefill_nvfp4", "qpn_lmhead_nvfp4"):
+        if name not in ("qpn_gemm_nvfp4", "qpn_gemm_prefill_nvfp4", "qpn_lmhead_nvfp4", "qpn_lmhead_verify_nvfp4"):
             return f
 
         def call(*args):
-            self.given.append(args[-3].value)      # .., workspace, its bytes, stream
-            return f(*args)
+            ws = args[-3].value                    # .., workspace, its bytes, stream
+            self.given.append(ws)
+            if self.launch:
+                return f(*args)
+            self.clashes += ws in self.inside
+            self.inside.append(ws)
+            time.sleep(0.002)                      # (another thread may run)
+            self.inside.remove(ws)
+            return 0
         return call
 
 
@@ -99,3 +110,33 @@ def test_a_stream_whose_first_calls_are_captured(calls):
         g.replay()
         same(out, want)
         same(all_of(stream), want)
+
+
+def test_threads_do_not_share_the_argmax_keys_at_the_same_time(monkeypatch):
+    # the lm_head's second launch reads the rows' keys from the workspace: on one stream, the launches of
+    # two threads' calls must not come in turn
+    qpn = need_gpu()
+    n, k = 512, 1024
+    pw = qpn.pack_nvfp4(dev(synth.weights(n, k, seed=7)))
+    x, draft = dev(synth.activations(4, k, seed=8)), torch.zeros(3, dtype=torch.int32, device="cuda")
+    stream = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    qpn.lmhead_nvfp4(pw, x, stream=stream)
+    torch.cuda.synchronize()
+    watch = Given(qpn.lib, launch=False)
+    monkeypatch.setattr(qpn, "lib", watch)
+    failed = []
+
+    def work(f):
+        try:
+            for _ in range(10):
+                f()
+        except Exception as e:  # noqa: BLE001
+            failed.append(e)
+    threads = [threading.Thread(target=work, args=(f,)) for f in (
+        lambda: qpn.lmhead_nvfp4(pw, x, stream=stream), lambda: qpn.lmhead_verify_nvfp4(pw, x, draft, stream=stream))]
+    for th in threads:
+        th.start()
+    for th in threads:
+        th.join()
+    assert not failed and len(watch.given) == 20 and watch.clashes == 0
