@@ -226,7 +226,8 @@ def rope_append(cache: KvCache, qkv, q_heads: int, positions, slots, inv_freq, q
         raise ValueError(f"out must be [{rows}, {q_heads * d}]")
     f16, i32 = torch.float16, torch.int32
     check(lib.qpn_kv_rope_append(
-        cache._ref or cache._checked(), qp, qs, rows, q_heads, None if q_weight is None else _need(q_weight, f16, 1, "q_weight"),
+        cache._ref or cache._checked(), qp, qs, rows, q_heads,
+        None if q_weight is None else _need(q_weight, f16, 1, "q_weight"),
         None if k_weight is None else _need(k_weight, f16, 1, "k_weight"), eps,
         None if inv_freq is None else _need(inv_freq, torch.float32, 1, "inv_freq"),
         0 if inv_freq is None else 2 * inv_freq.shape[0], interleaved, _need(positions, i32, 1, "positions"),
@@ -264,6 +265,8 @@ def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scal
         if scratch_ is None:
             need = attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
             scratch_ = _buffers.get(need if need < 1 << 63 else 0, key, stream)
+        else:
+            _need(scratch_, torch.uint8, 1, "scratch_")
         check(lib.qpn_kv_attention(
             cache._ref or cache._checked(), qp, qs, yp, ys, heads, shape[0], n, max_rows,
             _need(row_start, torch.int32, 1, "row_start"), _need(seq_lens, torch.int32, 1, "seq_lens"), tp, tstride,
@@ -305,6 +308,8 @@ def verify_sampled(logits, tokens, row_start, accept_u, sample_u, draft_logits=N
         if scratch_ is None:
             need = verify_scratch_bytes(rows, requests, n)
             scratch_ = _buffers.get(need if need < 1 << 63 else 0, key, stream)
+        else:
+            _need(scratch_, torch.uint8, 1, "scratch_")
         check(lib.qpn_kv_verify_sampled(
             lp, ls, dp or None, ds, _need(tokens, i32, 1, "tokens"), _need(row_start, i32, 1, "row_start"), rows,
             requests, n, 1.0 / temperature, _need(accept_u, f32, 1, "accept_u"),

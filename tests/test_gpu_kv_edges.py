@@ -275,3 +275,21 @@ def test_scratch_that_grows_within_a_capture(kv):
         for i, o in enumerate(outs):
             assert np.array_equal(host(o), calls[i % 2][1])
         assert np.array_equal(host(calls[0][0]()), calls[0][1])
+
+
+def test_scratch_that_is_given_is_checked(kv):
+    c = AttnCase(kv, [(2, 100)], 4, 2, 64, 66)
+    args = (c.device(), dev(c.q.reshape(2, -1)), i32(c.row_start), i32(c.seq), i32(c.table), 2)
+    _, _, verify = verify_case(kv, [2], 100, 67, False)
+    size = kv.SCRATCH_ZEROED + (1 << 20)
+    for bad in (torch.zeros(size, dtype=torch.uint8),                                   # on the host
+                torch.zeros(size, dtype=torch.float32, device="cuda"),
+                torch.zeros(2, size, dtype=torch.uint8, device="cuda"),
+                torch.zeros(2 * size, dtype=torch.uint8, device="cuda")[::2]):
+        with pytest.raises(ValueError, match="scratch"):
+            kv.attention(*args, scratch_=bad)
+        with pytest.raises(ValueError, match="scratch"):
+            kv.verify_sampled(*verify, scratch_=bad)
+    s = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    assert np.array_equal(host(kv.attention(*args, scratch_=s)).reshape(c.q.shape), c.run())
+    assert int(s[:kv.SCRATCH_ZEROED].count_nonzero()) == 0
