@@ -21,7 +21,7 @@ from functools import lru_cache
 
 import torch
 
-from .qpn import LIB_PATH, QpnError, StreamBuffers, _empty, _torch_stream, check, lib  # noqa: F401
+from .qpn import StreamBuffers, _empty, _torch_stream, check, lib
 
 PAGE = 64
 SCRATCH_ZEROED = 65536
@@ -100,11 +100,6 @@ def _raw_stream(stream) -> int:
 _buffers = StreamBuffers(SCRATCH_ZEROED, SCRATCH_ZEROED)
 _scratches, _locks = _buffers.held, _buffers.locks
 _unlocked = nullcontext()  # for a call that is given its scratch
-
-
-def scratch(nbytes: int, device, stream) -> torch.Tensor:
-    """The scratch of at least nbytes for `stream` (a torch stream) on `device`."""
-    return _buffers.get(nbytes, (torch.device(device).index, stream.cuda_stream), stream)
 
 
 class KvCache:
