@@ -15,7 +15,8 @@
 // are read: 16 bytes a lane, over whole lines.  The running maximum of a row is
 // only raised when a score exceeds it by more than 2^8 (weights up to 2^8 fit
 // FP16 as well as those up to 1), so most pages cost no exchange between lanes
-// and no rescaling.
+// and no rescaling.  FP16 weights, the second product's input, are off by 2^-11 of
+// each (below 2^-14 by 2^-25), as far as the output is by its own rounding.
 //
 // Two forms, by the rows of a KV head:
 //   few rows (up to kFewTiles tiles): each wavefront takes pages of its own,
@@ -786,11 +787,13 @@ __device__ __forceinline__ void join_pieces(const AttentionArgs& a, const AttnLa
 // pages.  The next keys are on their way once this page's are used, the next
 // values of a page once its present ones are.
 //
-// Bound: the cache's bytes when there is enough of it (8 rows of 40 + 8 heads of
-// 128 over 131001 tokens, 268 MB, not in any cache: 81.6 us, 3.3 TB/s, where a
-// large copy reaches 4.9; a step of eight pages keeps 128 KiB a CU on its way).
-// Short calls are bound by their chain of dependent steps: launch, table, keys,
-// values, hand-over, join (200 tokens 8.6 us, 4099 tokens 19.0 us).
+// Bound: over long caches the steps of eight pages, whose weights and values are
+// apart by a barrier (8 rows of 40 + 8 heads of 128 over 131001 tokens, 269 MB, not
+// in any cache: 81.0 us, 3.3 TB/s, where a large copy reaches 4.9 and a reduction
+// reads 5.8; from a graph, with part of it cached, 72.7 us, one row 51.9: the
+// bytes alone are not it).  Short calls are bound by their chain of dependent
+// steps: launch, table, keys, values, hand-over, join (200 tokens 8.8 us; 4099
+// tokens, nine pieces a head, 18.9 us).
 // ---------------------------------------------------------------------------
 template <int DIM, int RT>
 struct FewLds {
@@ -1065,8 +1068,8 @@ __global__ __launch_bounds__(few_waves(DIM) * 64) void attention_few_kernel(Atte
 // dimension 256 the ring does not fit, and they come through registers.
 //
 // Bound: the matrix and vector units of a SIMD, which two wavefronts share (256
-// rows of 40 + 8 heads of 128 over 20001 tokens, 104 GFLOP: 132 us with the join's
-// 8.8, 790 TFLOP/s, where a large FP16 matrix product reaches 1157).
+// rows of 40 + 8 heads of 128 over 20001 tokens, 104 GFLOP: 133 us with the join's
+// 8.9, 782 TFLOP/s, where a large FP16 matrix product reaches 1157).
 // ---------------------------------------------------------------------------
 constexpr int kRing = 4;
 

@@ -161,10 +161,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_round_kernel(PlanRoundArgs 
 // dependent loads, so what a page most likely needs (the rows that follow its
 // first one, the old codes) is fetched before it is known to be needed.
 //
-// Bound: one row 8.0 us, 8 rows 7.8 us (40 + 2 x 8 heads of 128): slots, rows,
-// 64-bit angles and codes one after another, of which the angles and norms are
-// 2 us.  4 x 256 rows of prompt blocks: 20 us (27 MB, 1.4 TB/s), the 64-bit
-// arithmetic of the keys (for about 10 us) beside the queries' 11.
+// Bound: one row and 8 rows 8.3 us (40 + 2 x 8 heads of 128; 6.7 from a graph, 3.0
+// of them with nothing to append): slots, rows, 64-bit angles, norms and codes one
+// after another.  4 x 256 rows of prompt blocks: 19.5 us (27 MB, 1.4 TB/s; 8.5
+// with nothing to append): 160 workgroups, of a page and KV head each, on 256 CUs,
+// with up to four such steps one after another; every one of them, and every
+// wavefront of queries, finds the angles of its rows by itself.
 // ---------------------------------------------------------------------------
 constexpr int kValuePitch = kKvPage + 4;
 
@@ -688,7 +690,7 @@ hipError_t launch_append(const RopeAppendArgs& a, int rows_per_wg) {
   constexpr int HPW = kLanes / (DIM / 8), WAVES = THREADS / kLanes;
   // heads per wavefront: one step of HPW while that leaves fewer wavefronts
   // than 8 a CU, else more, so that a row's angles serve more heads (1024 rows of
-  // one request: 18.1 us with one step each, 15.7 us so; 257 x 8 rows 58.4 and 49.9)
+  // one request: 18.3 us with one step each, 15.7 us so; 257 x 8 rows 58.5 and 49.9)
   const int head_groups = (a.q_heads + HPW - 1) / HPW;
   int64_t steps = (int64_t)a.rows * head_groups / 2048;
   steps = steps < 1 ? 1 : steps > head_groups ? head_groups : steps;
@@ -702,14 +704,17 @@ hipError_t launch_append(const RopeAppendArgs& a, int rows_per_wg) {
 }
 
 // Rows of a cache workgroup: one while those of all rows are about what the chip
-// holds at once, since each row may have a page of its own (64 requests of one
-// row and 8 heads: 10 us; with 16 rows a workgroup 78).  Above that many rows follow
-// others on their pages and most workgroups of one row would only look and
-// leave: eight (1024 prompt rows of one request: 31.6 us with one, 17.7 with four,
-// 15.8 with eight, 15.7 with 16; 300 requests of one row 43.7 us with four, 50.7
-// with eight, 79.7 with 16).  Pages of 256 dimensions then take eight wavefronts (2 x
-// 512 rows of 16 + 2 x 8 heads: 59.6 us with four, 40.1 with eight), the others four
-// (1024 rows of 128 dimensions: 15.9 and 17.4).
+// holds at once, since each row may have a page of its own (64 requests of one row
+// and 8 heads: 10 us; with 16 rows a workgroup 77).  Above that eight: rows of a
+// prompt follow others on their pages, and most workgroups of one row would only
+// look and leave.  With one, four, eight and 16: 1024 rows of one request 31.6,
+// 17.8, 15.7 and 15.6 us; 257 requests of 8 rows 134, 53, 50 and 48; but 300
+// requests of one row 36, 43, 51 and 79, and 1000 of them 110, 104, 102 and 102.
+// The host does not know how the rows lie on the pages, so the rule serves the
+// prompts, and batches of a few hundred single rows pay for it.  Pages of 256
+// dimensions take eight wavefronts then (2 x 512 rows of 16 + 2 x 8 heads: 29.6 us
+// with four, 21.9 with eight), the others four (1024 rows of 128 dimensions: 15.7
+// and 17.8).
 template <int DIM>
 hipError_t launch_append(const RopeAppendArgs& a) {
   if ((int64_t)a.rows * a.cache.heads <= 2048) return launch_append<DIM, 256>(a, 1);

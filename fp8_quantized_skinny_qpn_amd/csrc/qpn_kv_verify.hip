@@ -22,10 +22,12 @@
 //
 // Bound: the 64-bit arithmetic of the exponentials (some 20 operations each) next
 // to reading the logits: 32 requests of 8 rows of 151936 tokens, target and
-// drafter (156 MB, 78 million exponentials), take 100 us not in any cache, 70 of
-// them in the first kernel; at a large copy's rate the bytes alone would take 32.
-// 8 rows of a greedy drafter take 16 us: launch, one chunk a workgroup, the joins
-// of the last one and its search are each a chain of dependent steps.
+// drafter (156 MB, 78 million exponentials), take 88 to 100 us not in any cache, 70
+// of them in the first kernel; at a large copy's rate the bytes alone would take
+// 32.  The second one's 22 us are a launch, 32 rows of 38 chunks (19 MB), one a
+// workgroup, and their arrivals.  8 rows of a greedy drafter take 16 us: launch, one
+// chunk a workgroup, 304 arrivals on one counter, the joins of the last one and its
+// search, each waiting for the one before.
 //
 // What workgroups leave for one another is written through to the device's
 // point of coherence, and lies in 128-byte lines of one request alone: a line

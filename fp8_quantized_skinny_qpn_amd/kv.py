@@ -13,6 +13,11 @@ One round, on the device throughout::
     y = kv.attention(cache, q, r.row_start, r.seq_lens, table, max_rows)
     ...                                    # O, gate/up, down, lm_head
     accepted, token, prob = kv.verify_sampled(logits, tokens, r.row_start, accept_u, sample_u)
+
+Attention and verification pass sums on through a scratch that calls on one stream share, from any
+thread; calls captured into a graph share one of the graph's own, so graphs may run beside each
+other and beside calls.  A call may be given a scratch (`scratch_`, uint8): its first SCRATCH_ZEROED
+bytes zero before the first use, and no two calls at a time.
 """
 import ctypes
 from contextlib import nullcontext

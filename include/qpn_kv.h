@@ -98,7 +98,7 @@ QPN_API int qpn_kv_plan_round(const int32_t *before, const int32_t *rows, const 
  *   (a, b) -> (a cos t_j - b sin t_j, b cos t_j + a sin t_j) on the pair
  *   (j, j + rot / 2), or (2 j, 2 j + 1) when interleaved.
  * Queries go to q_out [rows, q_heads * dim] FP16 (row stride q_stride; q_out
- * may be qkv).  Keys and values of a row with a slot in [0, 64 * pages) go to
+ * may be qkv, with its stride).  Keys and values of a row with a slot in [0, 64 * pages) go to
  * the cache; other rows only write their queries.  Per page, head and kind:
  *   s = the smallest power of two with amax <= 448 s (at least 2^-60), amax
  *   over the finite new values; unless the page's first token (slot % 64 ==
@@ -106,9 +106,16 @@ QPN_API int qpn_kv_plan_round(const int32_t *before, const int32_t *rows, const 
  *   s grows the codes already there are rounded again to E4M3(code * old / s);
  *   new codes are E4M3(x / s), to nearest, ties to even, saturating, NaN to
  *   NaN.  Of two rows with one slot the later row counts.
- * Queries are computed in FP32 (angles reduced in FP64).  Keys are computed in
- * FP64 up to their codes, so a code differs from the definition's only where
- * the value is within ~1e-14 of a border between two codes.
+ * Queries are computed in FP32, with angles reduced in FP64 and the hardware's
+ * sine and cosine, which are off by up to 2^-20: before its rounding to FP16 a
+ * rotated query is off by some 2^-19 of its pair's length.  Keys are computed
+ * in FP64 up to their codes, so a key's code differs from the definition's only
+ * where its value is within 3e-14 of its pair's length of a border between two
+ * codes (position * inv_freq is exact for positions below 2^29 and rounded to
+ * 64 bits above).  Codes of values, and of keys neither normed nor rotated, are
+ * the definition's, for any scale that a page has.
+ * A page is written by one workgroup, which looks through all slots for its
+ * rows: the time of a call grows with rows times pages.
  * 0 <= rows <= 2^20, q_heads a multiple of the cache's heads (at most 64 each);
  * rows * (q_heads + heads) <= 2^30, rows * heads <= 2^25, eps >= 0.  Alignment:
  * qkv and q_out 16, weights 16, positions, slots 4. */
@@ -139,9 +146,13 @@ QPN_API size_t qpn_kv_attention_scratch_bytes(int requests, int max_rows, int q_
  * row_start is out of order or past `rows` are skipped; rows of no request are
  * not written.  max_rows: the most rows of one request, a hint that the tile
  * is chosen by.
- * Scores, weights' sums and outputs are held in FP32, the weights are rounded
- * to FP16 for the second product (error 2^-12 of each, averaged over the
- * tokens, next to the output's own 2^-12).  scale > 0, window >= 0.
+ * Scores, weights' sums and outputs are held in FP32.  For the second product
+ * each weight, in units in which a row's largest is from 1 to 2^8, is rounded
+ * to FP16: it is off by up to 2^-11 of itself, or 2^-25 where it is below
+ * 2^-14 (the output's own rounding: 2^-11).  With many rows a weight carries
+ * its page's value scale as a factor from 1 to 2^7 then, so it keeps at least
+ * these bits; values whose scale is below 2^-40 count as zeros there.
+ * scale > 0, window >= 0.
  * Deterministic.  0 <= rows <= 2^20, rows * q_heads <= 2^30, requests <= 4096. */
 QPN_API int qpn_kv_attention(const qpn_kv_cache *cache, const uint16_t *q, int64_t q_stride,
                              uint16_t *y, int64_t y_stride, int q_heads, int rows, int requests,
