@@ -182,8 +182,9 @@ QPN_API size_t qpn_kv_verify_scratch_bytes(int rows, int requests, int64_t n);
  * NaN or +inf, or nothing above -inf, refuses its draft (accept_prob NaN) and
  * gives next = -1; a draft row like that refuses it too, and next comes from
  * p.  A request without rows gives accepted 0, next -1.  All sums and
- * exponentials are FP64.  1 <= n <= 2^24, rows <= 65535, inv_temperature > 0
- * and finite; strides in elements.  One kernel for a greedy drafter, two for a
+ * exponentials are FP64, the latter off by up to 1.1e-12 of themselves.
+ * 1 <= n <= 2^24, rows <= 65535, inv_temperature > 0 and finite; strides in
+ * elements.  One kernel for a greedy drafter, two for a
  * sampled one. */
 QPN_API int qpn_kv_verify_sampled(const uint16_t *logits, int64_t logits_stride,
                                   const uint16_t *draft_logits, int64_t draft_stride,
