@@ -58,8 +58,9 @@ struct RopeAppendArgs {
 };
 hipError_t launch_rope_append(const RopeAppendArgs& a);
 
-struct AttentionArgs {
-  KvCache cache;
+template <typename Cache>
+struct AttentionOf {
+  Cache cache;
   const uint16_t* q;
   int64_t q_stride;
   uint16_t* y;
@@ -74,6 +75,7 @@ struct AttentionArgs {
   size_t scratch_bytes;
   void* stream;
 };
+using AttentionArgs = AttentionOf<KvCache>;
 size_t attention_scratch_bytes(int requests, int max_rows, int q_heads, int heads, int dim,
                                int table_width);
 hipError_t launch_attention(const AttentionArgs& a);
