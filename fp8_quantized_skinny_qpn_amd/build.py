@@ -26,7 +26,8 @@ SANITIZE_DIR = os.path.join(BUILD, "sanitize")
 SANITIZED_LIB = os.path.join(SANITIZE_DIR, "libqpn.so")
 
 SOURCES = ["qpn_api.cpp", "qpn_gemm.hip", "qpn_pack.hip", "qpn_prefill.hip",
-           "qpn_kv_api.cpp", "qpn_kv_round.hip", "qpn_kv_attn.hip", "qpn_kv_verify.hip"]
+           "qpn_kv_api.cpp", "qpn_kv_round.hip", "qpn_kv_attn.hip", "qpn_kv_verify.hip", "qpn_kv_logprobs.hip",
+           "qpn_kv4_cache.hip", "qpn_kv4_attn.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

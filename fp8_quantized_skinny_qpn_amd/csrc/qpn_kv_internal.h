@@ -27,6 +27,21 @@ struct KvCache {
   int dim;
 };
 
+// The 4-bit cache of one layer (layout: include/qpn_kv4.h).
+struct KvCache4 {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  const float* k_unit;
+  const float* v_unit;
+  int64_t pages;
+  int heads;
+  int dim;
+};
+__host__ __device__ constexpr int kv4_codes(int dim) { return kKvPage * dim / 2; }    // bytes of a block's codes
+__host__ __device__ constexpr int kv4_scales(int dim) { return kKvPage * dim / 16; }  // and of its scales
+
 struct PlanRoundArgs {
   const int32_t *before, *rows, *held;
   int requests;
@@ -42,8 +57,9 @@ struct PlanRoundArgs {
 };
 hipError_t launch_plan_round(const PlanRoundArgs& a);
 
-struct RopeAppendArgs {
-  KvCache cache;
+template <typename Cache>
+struct RopeAppendOf {
+  Cache cache;
   const uint16_t* qkv;
   int64_t qkv_stride;
   int rows, q_heads;
@@ -56,7 +72,22 @@ struct RopeAppendArgs {
   int64_t q_stride;
   void* stream;
 };
+using RopeAppendArgs = RopeAppendOf<KvCache>;
 hipError_t launch_rope_append(const RopeAppendArgs& a);
+using RopeAppend4Args = RopeAppendOf<KvCache4>;
+hipError_t launch_rope_append4(const RopeAppend4Args& a);
+
+struct Read4Args {
+  KvCache4 cache;
+  const int32_t* slots;
+  int rows;
+  uint16_t* k_out;
+  int64_t k_stride;
+  uint16_t* v_out;
+  int64_t v_stride;
+  void* stream;
+};
+hipError_t launch_read4(const Read4Args& a);
 
 template <typename Cache>
 struct AttentionOf {
@@ -79,6 +110,10 @@ using AttentionArgs = AttentionOf<KvCache>;
 size_t attention_scratch_bytes(int requests, int max_rows, int q_heads, int heads, int dim,
                                int table_width);
 hipError_t launch_attention(const AttentionArgs& a);
+using Attention4Args = AttentionOf<KvCache4>;
+size_t attention4_scratch_bytes(int requests, int max_rows, int q_heads, int heads, int dim,
+                                int table_width);
+hipError_t launch_attention4(const Attention4Args& a);
 
 struct VerifyArgs {
   const uint16_t* logits;
@@ -97,6 +132,24 @@ struct VerifyArgs {
 };
 size_t verify_scratch_bytes(int rows, int requests, int64_t n);
 hipError_t launch_verify(const VerifyArgs& a);
+
+constexpr int kLogprobsMaxTop = 32;
+struct LogprobsArgs {
+  const uint16_t* logits;
+  int64_t logits_stride;
+  const int32_t* tokens;
+  int rows;
+  int64_t n;
+  double inv_temperature;
+  int top;
+  float *logprob, *entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  void* scratch;
+  void* stream;
+};
+size_t logprobs_scratch_bytes(int rows, int64_t n);
+hipError_t launch_logprobs(const LogprobsArgs& a);
 
 // QPN_OK when the current device can run the library's kernels.
 int device_status();

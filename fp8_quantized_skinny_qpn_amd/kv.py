@@ -1,8 +1,9 @@
 """Thin ctypes binding of the speculative-round operators (the C ABI in include/qpn_kv.h).
 
 The operators around the packed-weight products of ``qpn``: page tables of a round, the cache
-append with query/key norms and rotation, attention over an 8-bit paged KV cache, and the
-verification of sampled drafts.  As in ``qpn``, argument marshalling only: every step of the
+append with query/key norms and rotation, attention over an 8-bit paged KV cache or a 4-bit one
+(include/qpn_kv4.h), reading the latter's tokens back, the verification of sampled drafts, and log
+probabilities.  As in ``qpn``, argument marshalling only: every step of the
 computation runs in the HIP kernels of libqpn.so, and there is no fallback of any kind.
 
 One round, on the device throughout::
@@ -13,8 +14,9 @@ One round, on the device throughout::
     y = kv.attention(cache, q, r.row_start, r.seq_lens, table, max_rows)
     ...                                    # O, gate/up, down, lm_head
     accepted, token, prob = kv.verify_sampled(logits, tokens, r.row_start, accept_u, sample_u)
+    logprob, entropy, ids, logprobs = kv.logprobs(logits, drafts, top=5)   # what a server answers with
 
-Attention and verification pass sums on through a scratch that calls on one stream share, from any
+Attention, verification and log probabilities pass sums on through a scratch that calls on one stream share, from any
 thread; calls captured into a graph share one of the graph's own, so graphs may run beside each
 other and beside calls.  A call may be given a scratch (`scratch_`, uint8): its first SCRATCH_ZEROED
 bytes zero before the first use, and no two calls at a time.
@@ -30,12 +32,18 @@ from .qpn import StreamBuffers, _empty, _torch_stream, check, lib
 
 PAGE = 64
 SCRATCH_ZEROED = 65536
+MAX_TOP = 32
 
 
 class _Cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p), ("pages", ctypes.c_int64), ("heads", ctypes.c_int32),
                 ("dim", ctypes.c_int32)]
+
+
+class _Cache4(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v", "k_scale", "v_scale", "k_unit", "v_unit")] + [
+        ("pages", ctypes.c_int64), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32)]
 
 
 def _bind():
@@ -51,16 +59,24 @@ def _bind():
         "qpn_kv_verify_scratch_bytes": ([i32, i32, i64], sz),
         "qpn_kv_verify_sampled": ([vp, i64, vp, i64, vp, vp, i32, i32, i64, f64, vp, vp, vp, vp, vp, vp, sz, vp],
                                   i32),
+        "qpn_kv_logprobs_scratch_bytes": ([i32, i64], sz),
+        "qpn_kv_logprobs": ([vp, i64, vp, i32, i64, f64, i32, vp, vp, vp, vp, vp, sz, vp], i32),
     }
-    for name, (args, res) in sig.items():
+    sig4 = {
+        "qpn_kv4_read": ([c.POINTER(_Cache4), vp, i32, vp, i64, vp, i64, vp], i32),
+    }
+    for name in ("rope_append", "attention_scratch_bytes", "attention"):
+        args, res = sig["qpn_kv_" + name]
+        sig4["qpn_kv4_" + name] = ([c.POINTER(_Cache4) if t is cp else t for t in args], res)
+    for name, (args, res) in (*sig.items(), *sig4.items()):
         f = getattr(lib, name)
         f.argtypes = args
         f.restype = res
-    return tuple(sig)
+    return tuple(sig), tuple(sig4)
 
 
-# Symbols the C header declares.
-EXPORTED = _bind()
+# Symbols the C headers declare (qpn_kv.h, qpn_kv4.h).
+EXPORTED, EXPORTED4 = _bind()
 
 
 def _need(t, dtype, dim, what):
@@ -98,7 +114,7 @@ def _raw_stream(stream) -> int:
     return stream.cuda_stream
 
 
-# Scratch of attention and verification: its zeroed head is left zero by every
+# Scratch of attention, verification and log probabilities: its zeroed head is left zero by every
 # call, the rest holds anything.  A call of several launches passes its sums on
 # through the scratch, so a call holds its scratch's lock until all of them are
 # queued: threads that share a stream queue whole calls one after another.
@@ -147,6 +163,67 @@ class KvCache:
         return cls(torch.zeros((pages, heads, dim // 16, PAGE, 16), dtype=f8, device=device),
                    torch.zeros((pages, heads, dim, PAGE), dtype=f8, device=device),
                    torch.ones((pages, heads), device=device), torch.ones((pages, heads), device=device))
+
+
+    _append, _attention = "qpn_kv_rope_append", "qpn_kv_attention"
+
+    @staticmethod
+    def _scratch_bytes(*sizes):
+        return attention_scratch_bytes(*sizes)
+
+
+class KvCache4(KvCache):
+    """One layer's cache in 4 bits: pages of 64 tokens, E2M1 codes with an E4M3 scale per token, head and
+    16 dimensions, and a float32 unit per head (a value is code * scale * unit; layout: include/qpn_kv4.h).
+
+    k, v: uint8 [pages, heads, dim / 32, 64, 16]; k_scale: float8_e4m3fn [pages, heads, 64, dim / 16];
+    v_scale: float8_e4m3fn [pages, heads, dim / 64, 16, 16]; k_unit, v_unit: float32 [heads], positive:
+    2688 units are the largest value, and a group whose largest is below 0.09 units has a coarser scale.
+    Setting a field takes effect at the next call."""
+
+    def __init__(self, k, v, k_scale, v_scale, k_unit, v_unit):
+        self.k_unit, self.v_unit = k_unit, v_unit
+        super().__init__(k, v, k_scale, v_scale)
+
+    def __setattr__(self, name, value):
+        if name == "k":
+            if value.dim() != 5 or value.shape[3] != PAGE or value.shape[4] != 16:
+                raise ValueError("keys must be [pages, heads, dim / 32, 64, 16]")
+            self.__dict__.update(pages=value.shape[0], heads=value.shape[1], dim=value.shape[2] * 32)
+        self.__dict__["_ref"] = None
+        self.__dict__[name] = value
+
+    def _checked(self):
+        if self._ref is None:
+            pages, heads, dim = self.pages, self.heads, self.dim
+            u8, f8, f32 = torch.uint8, torch.float8_e4m3fn, torch.float32
+            if self.v.shape != self.k.shape:
+                raise ValueError("values must have the keys' shape")
+            if tuple(self.k_scale.shape) != (pages, heads, PAGE, dim // 16) \
+                    or tuple(self.v_scale.shape) != (pages, heads, dim // 64, 16, 16):
+                raise ValueError("scales must be [pages, heads, 64, dim / 16] and [pages, heads, dim / 64, 16, 16]")
+            if tuple(self.k_unit.shape) != (heads,) or tuple(self.v_unit.shape) != (heads,):
+                raise ValueError("units must be [heads]")
+            self.__dict__["_ref"] = ctypes.byref(_Cache4(
+                _need(self.k, u8, 5, "keys"), _need(self.v, u8, 5, "values"), _need(self.k_scale, f8, 4, "key scales"),
+                _need(self.v_scale, f8, 5, "value scales"), _need(self.k_unit, f32, 1, "key units"),
+                _need(self.v_unit, f32, 1, "value units"), pages, heads, dim))
+        return self._ref
+
+    @classmethod
+    def empty(cls, pages: int, heads: int, dim: int, device="cuda", unit: float = 0.125) -> "KvCache4":
+        """A cache of pages no request holds yet."""
+        z = lambda dtype, *s: torch.zeros((pages, heads) + s, dtype=torch.uint8, device=device).view(dtype)  # noqa: E731
+        u8, f8 = torch.uint8, torch.float8_e4m3fn
+        return cls(z(u8, dim // 32, PAGE, 16), z(u8, dim // 32, PAGE, 16), z(f8, PAGE, dim // 16),
+                   z(f8, dim // 64, 16, 16), torch.full((heads,), unit, dtype=torch.float32, device=device),
+                   torch.full((heads,), unit, dtype=torch.float32, device=device))
+
+    _append, _attention = "qpn_kv4_rope_append", "qpn_kv4_attention"
+
+    @staticmethod
+    def _scratch_bytes(*sizes):
+        return attention4_scratch_bytes(*sizes)
 
 
 @dataclass
@@ -207,7 +284,8 @@ def plan_round(before, rows, held, table, free_pages, free_count, capacity: int 
 
 def rope_append(cache: KvCache, qkv, q_heads: int, positions, slots, inv_freq, q_weight=None, k_weight=None,
                 eps: float = 1e-6, interleaved: bool = False, out=None, stream=None) -> torch.Tensor:
-    """Norms, rotation and cache append of QKV rows through qpn_kv_rope_append; returns the queries
+    """Norms, rotation and cache append of QKV rows through qpn_kv_rope_append (qpn_kv4_rope_append
+    for a KvCache4); returns the queries
     [rows, q_heads * dim].  inv_freq: float32 [rot / 2] (None: no rotation)."""
     d = cache.dim
     rows = qkv.shape[0]
@@ -225,7 +303,7 @@ def rope_append(cache: KvCache, qkv, q_heads: int, positions, slots, inv_freq, q
     if tuple(out.shape) != (rows, q_heads * d):
         raise ValueError(f"out must be [{rows}, {q_heads * d}]")
     f16, i32 = torch.float16, torch.int32
-    check(lib.qpn_kv_rope_append(
+    check(getattr(lib, cache._append)(
         cache._ref or cache._checked(), qp, qs, rows, q_heads,
         None if q_weight is None else _need(q_weight, f16, 1, "q_weight"),
         None if k_weight is None else _need(k_weight, f16, 1, "k_weight"), eps,
@@ -235,14 +313,39 @@ def rope_append(cache: KvCache, qkv, q_heads: int, positions, slots, inv_freq, q
     return out
 
 
+def read(cache: KvCache4, slots, out=None, stream=None):
+    """(keys, values) float16 [rows, heads * dim] of the tokens slots [rows] through qpn_kv4_read: what the
+    cache holds for them; zeros for a slot outside the cache."""
+    if not isinstance(cache, KvCache4):
+        raise TypeError("tokens are read back from a KvCache4")
+    rows, width = slots.shape[0], cache.heads * cache.dim
+    sp = _need(slots, torch.int32, 1, "slots")
+    if out is None:
+        ts = _torch_stream(stream)
+        out = (_empty(ts, (rows, width), torch.float16, slots.device),
+               _empty(ts, (rows, width), torch.float16, slots.device))
+    k, v = out
+    if tuple(k.shape) != (rows, width) or tuple(v.shape) != (rows, width):
+        raise ValueError(f"out must be two of [{rows}, {width}]")
+    (kp, ks), (vp, vs) = _rows(k, "out"), _rows(v, "out")
+    check(lib.qpn_kv4_read(cache._ref or cache._checked(), sp, rows, kp, ks, vp, vs, _raw_stream(stream)))
+    return out
+
+
 @lru_cache(maxsize=1024)
 def attention_scratch_bytes(requests: int, max_rows: int, q_heads: int, heads: int, dim: int, width: int) -> int:
     return int(lib.qpn_kv_attention_scratch_bytes(requests, max_rows, q_heads, heads, dim, width))
 
 
+@lru_cache(maxsize=1024)
+def attention4_scratch_bytes(requests: int, max_rows: int, q_heads: int, heads: int, dim: int, width: int) -> int:
+    return int(lib.qpn_kv4_attention_scratch_bytes(requests, max_rows, q_heads, heads, dim, width))
+
+
 def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scale: float = None, window: int = 0,
               out=None, stream=None, scratch_=None) -> torch.Tensor:
-    """Attention of the rows q [rows, q_heads * dim] over the cache through qpn_kv_attention.
+    """Attention of the rows q [rows, q_heads * dim] over the cache through qpn_kv_attention
+    (qpn_kv4_attention for a KvCache4).
     `max_rows`: the most rows of one request (a hint).  `scale` defaults to dim ** -0.5."""
     d = cache.dim
     n = seq_lens.shape[0]
@@ -263,11 +366,11 @@ def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scal
     key = (q.get_device(), raw)
     with _locks[key] if scratch_ is None else _unlocked:
         if scratch_ is None:
-            need = attention_scratch_bytes(n, max_rows, heads, cache.heads, d, width)
+            need = cache._scratch_bytes(n, max_rows, heads, cache.heads, d, width)
             scratch_ = _buffers.get(need if need < 1 << 63 else 0, key, stream)
         else:
             _need(scratch_, torch.uint8, 1, "scratch_")
-        check(lib.qpn_kv_attention(
+        check(getattr(lib, cache._attention)(
             cache._ref or cache._checked(), qp, qs, yp, ys, heads, shape[0], n, max_rows,
             _need(row_start, torch.int32, 1, "row_start"), _need(seq_lens, torch.int32, 1, "seq_lens"), tp, tstride,
             width, d ** -0.5 if scale is None else scale, window, scratch_.data_ptr(), scratch_.numel(), raw))
@@ -315,4 +418,45 @@ def verify_sampled(logits, tokens, row_start, accept_u, sample_u, draft_logits=N
             requests, n, 1.0 / temperature, _need(accept_u, f32, 1, "accept_u"),
             _need(sample_u, f32, 1, "sample_u"), _need(accepted, i32, 1, "accepted"), _need(token, i32, 1, "next"),
             _need(prob, f32, 1, "accept_prob"), scratch_.data_ptr(), scratch_.numel(), raw))
+    return out
+
+
+@lru_cache(maxsize=1024)
+def logprobs_scratch_bytes(rows: int, n: int) -> int:
+    return int(lib.qpn_kv_logprobs_scratch_bytes(rows, n))
+
+
+def logprobs(logits, tokens, top: int = 0, temperature: float = 1.0, out=None, stream=None, scratch_=None):
+    """(logprob float32 [rows], entropy float32 [rows], top_ids int32 [rows, top], top_logprobs float32
+    [rows, top]) through qpn_kv_logprobs: the log probabilities of tokens [rows] under
+    softmax(logits / temperature), its entropy, and the likeliest tokens (equal ones: the lowest first)."""
+    rows, n = logits.shape
+    lp, ls = _rows(logits, "logits")
+    if tokens.shape[0] != rows:
+        raise ValueError("tokens must have one entry per row")
+    if not temperature > 0:
+        raise ValueError("temperature must be positive")
+    if not 0 <= top <= min(n, MAX_TOP):
+        raise ValueError(f"top must be from 0 to {min(n, MAX_TOP)}")
+    raw = _raw_stream(stream)
+    dev, i32, f32 = logits.device, torch.int32, torch.float32
+    if out is None:
+        ts = _torch_stream(stream)
+        out = (_empty(ts, (rows,), f32, dev), _empty(ts, (rows,), f32, dev), _empty(ts, (rows, top), i32, dev),
+               _empty(ts, (rows, top), f32, dev))
+    logprob, entropy, ids, alternatives = out
+    if logprob.shape[0] != rows or entropy.shape[0] != rows or tuple(ids.shape) != (rows, top) \
+            or tuple(alternatives.shape) != (rows, top):
+        raise ValueError("out must be (logprob [rows], entropy [rows], top_ids [rows, top], top_logprobs [rows, top])")
+    key = (logits.get_device(), raw)
+    with _locks[key] if scratch_ is None else _unlocked:
+        if scratch_ is None:
+            need = logprobs_scratch_bytes(rows, n)
+            scratch_ = _buffers.get(need if need < 1 << 63 else 0, key, stream)
+        else:
+            _need(scratch_, torch.uint8, 1, "scratch_")
+        check(lib.qpn_kv_logprobs(
+            lp, ls, _need(tokens, i32, 1, "tokens"), rows, n, 1.0 / temperature, top,
+            _need(logprob, f32, 1, "logprob"), _need(entropy, f32, 1, "entropy"), _need(ids, i32, 2, "top_ids"),
+            _need(alternatives, f32, 2, "top_logprobs"), scratch_.data_ptr(), scratch_.numel(), raw))
     return out

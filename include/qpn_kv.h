@@ -1,8 +1,9 @@
 /*
  * qpn_kv.h -- C ABI of the operators of a speculative round that stand around
  * the packed-weight products of qpn.h: page tables, the cache append with
- * query/key norms and rotation, attention over an 8-bit paged KV cache, and
- * the verification of sampled drafts.  MI355X (gfx950).
+ * query/key norms and rotation, attention over an 8-bit paged KV cache, the
+ * verification of sampled drafts, and the log probabilities that a server answers
+ * with.  MI355X (gfx950).  The operators of a 4-bit cache: qpn_kv4.h.
  *
  * One round on the device, without a host read:
  *   qpn_kv_plan_round      rows and lengths of the requests -> page tables,
@@ -13,6 +14,7 @@
  *   qpn_kv_attention       the rows against the cache
  *   (O, gate/up, down, lm_head products)
  *   qpn_kv_verify_sampled  accepted drafts and the next token
+ *   qpn_kv_logprobs        log probabilities of tokens, entropy, alternatives
  *
  * The cache of one layer.  Pages of QPN_KV_PAGE = 64 tokens; per page and KV
  * head the keys and the values are one block each of 64 * dim E4M3 codes
@@ -35,7 +37,7 @@
  * Rows of the requests lie one after another: request r has rows
  * row_start[r] .. row_start[r + 1] - 1.
  *
- * Scratch.  Attention and verification take device scratch of their own
+ * Scratch.  Attention, verification and log probabilities take device scratch of their own
  * (16-byte aligned; not the workspace of qpn.h): its first
  * QPN_KV_SCRATCH_ZEROED bytes must be zero before its first use and every call
  * leaves them zero; the rest may hold anything.  Calls that share a scratch
@@ -193,6 +195,34 @@ QPN_API int qpn_kv_verify_sampled(const uint16_t *logits, int64_t logits_stride,
                                   const float *accept_u, const float *sample_u, int32_t *accepted,
                                   int32_t *next, float *accept_prob, void *scratch,
                                   size_t scratch_bytes, void *stream);
+
+#define QPN_KV_MAX_TOP 32
+
+/* Bytes of scratch qpn_kv_logprobs needs ((size_t)-1 for sizes out of range).
+ * Pure host. */
+QPN_API size_t qpn_kv_logprobs_scratch_bytes(int rows, int64_t n);
+
+/* Log probabilities.  With p = softmax(inv_temperature * logits[row]) over the n
+ * tokens of a row:
+ *   logprob[row] = log p(tokens[row]),   entropy[row] = - sum p log p,
+ *   top_ids[row][0 .. top - 1] and top_logprobs: the `top` tokens of the largest
+ *   logits in falling order, of equal ones (-0 and 0 are) the lowest index first,
+ *   and their log p.
+ * A token outside 0 .. n - 1 has the log probability NaN; a logit of -inf has the
+ * probability 0 and the log probability -inf.  A row with NaN or +inf, or nothing above
+ * -inf, gives NaN throughout and ids of -1.
+ * Exponentials are FP32, off by up to 2^-23 (1 + |x|) of themselves for exp(x); their
+ * sum is FP64 and held so that a token's probability near 1 keeps a relative precision
+ * of its distance from 1; results are rounded to FP32.  Deterministic but for
+ * the order of a row's pieces, which is fixed too.
+ * 0 <= rows <= 65535, 1 <= n <= 2^24, 0 <= top <= min(n, QPN_KV_MAX_TOP) (top_ids and
+ * top_logprobs may be NULL when 0), inv_temperature > 0 and finite.  logits need
+ * no more than their 2-byte alignment; rows at multiples of 16 bytes are as fast as
+ * others but for their ends.  One kernel. */
+QPN_API int qpn_kv_logprobs(const uint16_t *logits, int64_t logits_stride, const int32_t *tokens,
+                            int rows, int64_t n, double inv_temperature, int top, float *logprob,
+                            float *entropy, int32_t *top_ids, float *top_logprobs, void *scratch,
+                            size_t scratch_bytes, void *stream);
 
 #ifdef __cplusplus
 }
