@@ -208,6 +208,30 @@ __device__ __forceinline__ void load_query(const Attention4Args& a, const AttnLa
     q[k] = in ? *reinterpret_cast<const half8*>(src + 8 * k) : half8{};
 }
 
+// -inf for what a row does not see of half a page's scores; the largest of a lane's eight.
+template <int RT>
+__device__ __forceinline__ void mask_half(float4v (&x)[2][RT], int base, int g, const View<RT>& see) {
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    const uint32_t seen = seen_of(see.lim[rt], see.low(rt), base, g);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const uint32_t ones = all_ones_if(seen, t, r);
+        const float y = x[t][rt][r];  // (a bit cast of an element itself reads the vector's first one)
+        x[t][rt][r] = __builtin_bit_cast(float, (__builtin_bit_cast(uint32_t, y) & ones) | (0xFF800000u & ~ones));
+      }
+  }
+}
+template <int RT>
+__device__ __forceinline__ float half_max(const float4v (&x)[2][RT], int rt) {
+  float mx = fmaxf(x[0][rt][0], x[0][rt][1]);
+#pragma unroll
+  for (int i = 2; i < 8; i += 2) mx = fmaxf(fmaxf(mx, x[i >> 2][rt][i & 3]), x[i >> 2][rt][(i & 3) + 1]);
+  return mx;
+}
+
 // ---------------------------------------------------------------------------
 // Few rows: each wavefront takes pages of its own, all rows of the segment, straight
 // into registers; the workgroup's wavefronts are joined through LDS at the end.
@@ -253,6 +277,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void attention4_few_kernel(Attentio
     if (wave < RT) load_query<DIM>(a, l, q, it.head, lane, row_first, rows_here, wave, qr);
     int ids = load_ids(a, table, q.bad, lane, lo, W, hi);
     const float factor = unit_of(a.cache.k_unit, it.head) * (a.scale * 1.44269504088896340736f);
+    // (positive and finite, so that -inf stays what it is)
+    const float kc = fminf(fmaxf(factor, 0x1p-126f), 0x1p127f);
     const float v_unit = unit_of(a.cache.v_unit, it.head);
 
     Keys<DIM> k;
@@ -268,98 +294,99 @@ __global__ __launch_bounds__(kFewWaves * 64) void attention4_few_kernel(Attentio
     }
     lds_barrier();
 
-    float m[RT], sum[RT];
-    float4v o[DT][RT];
+    float m[RT];
+    float4v o[DT][RT], sum[RT];  // (the weights' sums by the matrix unit, too: all four the same)
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       m[rt] = kLowest;
-      sum[rt] = 0.0f;
+      sum[rt] = float4v{0, 0, 0, 0};
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d][rt] = float4v{0, 0, 0, 0};
     }
+    const half8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
 
 #pragma unroll 1
     for (int i0 = 0; i0 < count; ++i0) {
       const int base = (lo + i0 * W) * kKvPage;
-      const float kc = id < 0 ? __builtin_nanf("") : factor;
+      const float none_factor = id < 0 || factor != factor ? __builtin_nanf("") : 1.0f;  // no page, or no unit
       // the next page (the last one again behind it)
       if (((i0 + 1) & 63) == 0) ids = load_ids(a, table, q.bad, lane, lo + (i0 + 1) * W, W, hi);
       const int next = i0 + 1 < count ? __builtin_amdgcn_readlane(ids, (i0 + 1) & 63) : id;
       const int64_t next_block = block_of(a, it.head, next);
+      const bool edge = base + kKvPage > see.lim_min || base < see.low_max;
+      if (edge) v.template clean<RT>(base, g, see, o);
+      const float kp = edge ? kc : kc * none_factor;  // (at the edge NaN only for rows that see the page)
 
-      float4v x[4][RT];
+      // by halves of the page, 32 tokens, a k-step of the second product
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+      for (int h = 0; h < 2; ++h) {
+        float4v x[2][RT];
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) x[t][rt] = float4v{0, 0, 0, 0};
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < G; ++i)
+          for (int rt = 0; rt < RT; ++rt) x[t][rt] = float4v{0, 0, 0, 0};
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
+        for (int k0 = 0; k0 < KS; ++k0) {
           half8 qf[RT];
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) qf[rt] = s.q[2 * i + h][rt][lane];
+          for (int rt = 0; rt < RT; ++rt) qf[rt] = s.q[k0][rt][lane];
 #pragma unroll
-          for (int t = 0; t < 4; ++t) {
-            const half8 kf = k.operand(t, i, h);
+          for (int t = 0; t < 2; ++t) {
+            const half8 kf = k.operand(2 * h + t, k0 / 2, k0 % 2);
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
               x[t][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[rt], x[t][rt], 0, 0, 0);
           }
         }
-      k.load(a.cache, next_block, lane);
+        if (h == 1) k.load(a.cache, next_block, lane);
+        if (edge) {  // what a row does not see is -inf
+          asm volatile("; edge");  // (a branch, not a select of every score)
 #pragma unroll
-      for (int t = 0; t < 4; ++t)
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) x[t][rt] *= kc;
-      const bool edge = base + kKvPage > see.lim_min || base < see.low_max;
-      if (edge) mask_page<RT>(x, base, g, see);  // what a row does not see is -inf
-      float high[RT];
-      bool raise = false;
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        high[rt] = page_max<RT>(x, rt);
-        raise |= high[rt] > m[rt] + kMaxSlack;
-      }
-      if (__ballot(raise)) {
+            for (int rt = 0; rt < RT; ++rt) x[t][rt] *= none_factor;
+          mask_half<RT>(x, base + 32 * h, g, see);
+        }
+        float high[RT];
+        bool raise = false;
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          float mx = fmaxf(high[rt], __shfl_xor(high[rt], 16));
-          mx = fmaxf(mx, __shfl_xor(mx, 32));
-          const float up = fmaxf(m[rt], mx);
-          const float f = __builtin_amdgcn_exp2f(m[rt] - up);
-          sum[rt] *= f;
-          m[rt] = up;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) o[d][rt] *= f;
+          high[rt] = half_max<RT>(x, rt) * kp;
+          raise |= high[rt] > m[rt] + kMaxSlack;
         }
-      }
-      if (edge) v.template clean<RT>(base, g, see, o);
-      half8 p[2][RT];
+        if (__ballot(raise)) {
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        float part[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          for (int rt = 0; rt < RT; ++rt) {
+            float mx = fmaxf(high[rt], __shfl_xor(high[rt], 16));
+            mx = fmaxf(mx, __shfl_xor(mx, 32));
+            const float up = fmaxf(m[rt], mx);
+            const float f = __builtin_amdgcn_exp2f(m[rt] - up);
+            sum[rt] *= f;
+            m[rt] = up;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const float w = __builtin_amdgcn_exp2f(x[t][rt][r] - m[rt]);
-            part[t] += w;
-            x[t][rt][r] = w;
+            for (int d = 0; d < DT; ++d) o[d][rt] *= f;
           }
-        sum[rt] += (part[0] + part[1]) + (part[2] + part[3]);
-        p[0][rt] = to_half8(x[0][rt], x[1][rt]);
-        p[1][rt] = to_half8(x[2][rt], x[3][rt]);
-      }
+        }
+        half8 p[RT];
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              x[t][rt][r] = __builtin_amdgcn_exp2f(__builtin_fmaf(x[t][rt][r], kp, -m[rt]));
+          p[rt] = to_half8(x[0][rt], x[1][rt]);
+        }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sum[rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[rt], sum[rt], 0, 0, 0);
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
           const half8 vf = v.operand(d, h);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt)
-            o[d][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[h][rt], o[d][rt], 0, 0, 0);
+            o[d][rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, p[rt], o[d][rt], 0, 0, 0);
         }
+      }
       v.load(a.cache, next_block, lane);
       id = next;
     }
@@ -367,9 +394,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void attention4_few_kernel(Attentio
     // the wavefronts' sums against their common maximum
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      sum[rt] += __shfl_xor(sum[rt], 16);
-      sum[rt] += __shfl_xor(sum[rt], 32);
-      if (g == 0) s.m[rt * 16 + c16][wave] = m[rt], s.sum[rt * 16 + c16][wave] = sum[rt];
+      if (g == 0) s.m[rt * 16 + c16][wave] = m[rt], s.sum[rt * 16 + c16][wave] = sum[rt][0];
     }
     lds_barrier();
     const __amdgpu_buffer_rsrc_t res = partial_of(l);
