@@ -31,6 +31,18 @@ template <>
 struct KindOf<Attention4Args> {
   static constexpr int few_tiles(int dim) { return dim == 256 ? 1 : 3; }
   static constexpr int many_tiles(int dim) { return dim == 256 ? 1 : 2; }
+  // Several tiles of a KV head in one workgroup decode its codes once, but leave as many times
+  // the sums to join: with few segments, up to some length, a workgroup a tile is the faster
+  // one.  8 rows of 40 + 8 heads (three tiles) over 1000 / 5001 / 32000 / 64000 / 131001 tokens:
+  // together 15.6 / 19.5 / 30.5 / 38.3 / 56.8 us, apart 11.3 / 13.1 / 25.8 / 38.2 / 68.4; 3
+  // requests of them over up to 4000 21.0 and 21.1, 4 over up to 8000 27.5 and 28.5.  Where no
+  // segment is cut, while a workgroup each finds a CU: 10 requests over up to 500 tokens 15.3
+  // and 12.3, 16 of them 15.4 and 23.2.
+  static constexpr bool apart(int64_t tiles, int64_t groups, int64_t pages) {
+    return tiles * groups <= (pages <= kMinPiecePages ? 256 : 80) && tiles * groups * pages <= 24576;
+  }
+  static constexpr int at_once(int n) { return n >= 3 ? 4 : 8; }
+  static constexpr int kJoinDirect = 16;
   // lane group g of the accumulators holds dimensions 16 (G g + i) + 4 j + b, b = 0 .. 3,
   // of the dimension tile d = 4 i + j
   template <int DIM>
@@ -266,16 +278,22 @@ __global__ __launch_bounds__(kFewWaves * 64) void attention4_few_kernel(Attentio
     const int row_first = it.tile * ROWS;  // among the segment's rows
     const int rows_here = min(ROWS, q.rows * l.group - row_first);
     const View<RT> see = view_of<RT>(a, l, q, lane, row_first, rows_here);
-    // the piece's pages that the tile sees; this wavefront's are lo, lo + W, ...
-    const int lo = wave + max(q.first_page + (int)((int64_t)q.pages * it.piece / it.pieces), see.low_min / kKvPage);
-    const int hi = min(q.first_page + (int)((int64_t)q.pages * (it.piece + 1) / it.pieces),
+    // The piece's pages that the tile sees.  Of two wavefronts on a SIMD the older one issues
+    // first; with much to compute it is 5/3 as fast, and gets as many more pages: the older
+    // four the first part, the others the rest, each every fourth page.
+    const int first_page = max(q.first_page + (int)((int64_t)q.pages * it.piece / it.pieces), see.low_min / kKvPage);
+    const int end_page = min(q.first_page + (int)((int64_t)q.pages * (it.piece + 1) / it.pieces),
                        (see.lim_max + kKvPage - 1) / kKvPage);
-    const int count = hi > lo ? (hi - lo + W - 1) / W : 0;
+    constexpr int STEP = W / 2, SHARE = RT > 1 ? 5 : 4;  // (eighths)
+    const int all_pages = max(end_page - first_page, 0);
+    const int part = all_pages <= STEP ? all_pages : STEP * ((SHARE * all_pages + 4 * STEP) / (8 * STEP));
+    const int lo = first_page + (wave < STEP ? wave : part + wave - STEP), hi = wave < STEP ? first_page + part : end_page;
+    const int count = hi > lo ? (hi - lo + STEP - 1) / STEP : 0;
     const int32_t* const table = a.table + it.request * a.table_stride;
     static_assert(RT <= W, "a row tile of queries per wavefront");
     half8 qr[KS];
     if (wave < RT) load_query<DIM>(a, l, q, it.head, lane, row_first, rows_here, wave, qr);
-    int ids = load_ids(a, table, q.bad, lane, lo, W, hi);
+    int ids = load_ids(a, table, q.bad, lane, lo, STEP, hi);
     const float factor = unit_of(a.cache.k_unit, it.head) * (a.scale * 1.44269504088896340736f);
     // (positive and finite, so that -inf stays what it is)
     const float kc = fminf(fmaxf(factor, 0x1p-126f), 0x1p127f);
@@ -307,10 +325,10 @@ __global__ __launch_bounds__(kFewWaves * 64) void attention4_few_kernel(Attentio
 
 #pragma unroll 1
     for (int i0 = 0; i0 < count; ++i0) {
-      const int base = (lo + i0 * W) * kKvPage;
+      const int base = (lo + i0 * STEP) * kKvPage;
       const float none_factor = id < 0 || factor != factor ? __builtin_nanf("") : 1.0f;  // no page, or no unit
       // the next page (the last one again behind it)
-      if (((i0 + 1) & 63) == 0) ids = load_ids(a, table, q.bad, lane, lo + (i0 + 1) * W, W, hi);
+      if (((i0 + 1) & 63) == 0) ids = load_ids(a, table, q.bad, lane, lo + (i0 + 1) * STEP, STEP, hi);
       const int next = i0 + 1 < count ? __builtin_amdgcn_readlane(ids, (i0 + 1) & 63) : id;
       const int64_t next_block = block_of(a, it.head, next);
       const bool edge = base + kKvPage > see.lim_min || base < see.low_max;
@@ -340,12 +358,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void attention4_few_kernel(Attentio
         }
         if (h == 1) k.load(a.cache, next_block, lane);
         if (edge) {  // what a row does not see is -inf
-          asm volatile("; edge");  // (a branch, not a select of every score)
+          int gg = g;
+          asm volatile("; edge" : "+v"(gg));  // (all of this in the branch, not a select of every score)
 #pragma unroll
           for (int t = 0; t < 2; ++t)
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt) x[t][rt] *= none_factor;
-          mask_half<RT>(x, base + 32 * h, g, see);
+          mask_half<RT>(x, base + 32 * h, gg, see);
         }
         float high[RT];
         bool raise = false;

@@ -35,15 +35,16 @@ constexpr int kManyWaves = 8;  // and many rows
 // with 16; 256 rows over 4096: 46.3, 46.2, 53.2.)
 constexpr int kMinPiecePages = 8;
 constexpr int kMaxPieces = 512;    // pieces of a call with cut segments
-// Pieces joined in one step.  (8 rows over 16384 tokens, 32 pieces a head: 30.6 us
-// in one step, 26.0 us in two; over 131001 tokens 78.6 and 75.1 us.)
-constexpr int kJoinDirect = 16;
 constexpr int kCounterStep = 8;    // 32-bit words between counters
 static_assert((size_t)kMaxPieces * 2 * kCounterStep * 4 <= kKvZeroedBytes, "two counters per piece");
 
 // What differs between the caches, for a kind of arguments A:
 //   few_tiles(dim), many_tiles(dim)  16-row tiles: the most of the few-rows form, those of a
 //                                    wavefront with many rows
+//   apart(tiles, groups, pages)      whether the tiles of few rows are segments of their own, with
+//                                    so many requests x KV heads and pages of each at most
+//   at_once(n)                       sums of n fragments each that a join loads together
+//   kJoinDirect                      pieces joined in one step
 //   first_dim<DIM>(d, g)             the first of the four dimensions that lane group g holds of
 //                                    the dimension tile d of the second product
 template <typename A>
@@ -55,9 +56,10 @@ struct Form {
   int rows() const { return 16 * tiles * (many ? kManyWaves : 1); }
 };
 template <typename A>
-Form form_for(int64_t rows, int dim) {
-  const int64_t t = (rows + 15) / 16;
-  if (t <= KindOf<A>::few_tiles(dim)) return {false, t < 1 ? 1 : (int)t};
+Form form_of(int requests, int max_rows, int q_heads, int heads, int dim, int table_width) {
+  const int64_t t = ((int64_t)max_rows * (q_heads / heads) + 15) / 16;
+  if (t <= KindOf<A>::few_tiles(dim))
+    return {false, t < 1 || KindOf<A>::apart(t, (int64_t)requests * heads, table_width) ? 1 : (int)t};
   return {true, t <= kManyWaves ? 1 : KindOf<A>::many_tiles(dim)};
 }
 
@@ -103,10 +105,15 @@ __device__ __forceinline__ Req request_of(const A& a, const AttnLaunch& l, int r
   return q;
 }
 
+// The sum over the wavefront, in every lane: within 16 lanes by data-parallel moves (quad_perm
+// 1 0 3 2 and 2 3 0 1, mirrored within 8 and 16), then between the four rows.
 __device__ __forceinline__ int wave_sum(int x) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) x += __shfl_xor(x, d);
-  return x;
+  x += __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false);
+  x += __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false);
+  x += __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, false);
+  x += __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, false);
+  return (__builtin_amdgcn_readlane(x, 0) + __builtin_amdgcn_readlane(x, 16)) +
+         (__builtin_amdgcn_readlane(x, 32) + __builtin_amdgcn_readlane(x, 48));
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -478,6 +485,18 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
+// A load of 16 bytes a lane into LDS: lane i's go to lds + 16 i.
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)lds)), "v"(offset), "s"(base)
+               : "memory", "m0");
+}
+
+// The same with 4 bytes a lane, lane i's to lds + 4 i.
+__device__ __forceinline__ void word_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(uniform((int)lds)), "v"(offset), "s"(base)
+               : "memory", "m0");
+}
+
 template <int RT, typename A>
 __device__ __forceinline__ View<RT> view_of(const A& a, const AttnLaunch& l, const Req& q, int lane,
                                             int first, int rows) {
@@ -551,12 +570,11 @@ __device__ __forceinline__ bool arrive_last(uint32_t* counter, int n, uint32_t* 
 // Joins the fragments of A row tiles (rt0 on) and B dimension tiles (d0 on) of
 // `count` partial sums in order.  slot(i): the i-th one's slot.  The loads of
 // CH sums go out together.
-template <int DIM, int TILES, int A, int B, typename SlotOf>
+template <int DIM, int TILES, int A, int B, int CH, typename SlotOf>
 __device__ __forceinline__ void join_fragments(__amdgpu_buffer_rsrc_t res, int lane, int rt0, int d0, int count,
                                                const SlotOf& slot, float4v (&sum)[A][B], float (&top)[A],
                                                float (&weight)[A]) {
   using S = Slot<DIM, TILES>;
-  constexpr int CH = A * B >= 3 ? 4 : 8;
   const int c16 = lane & 15;
 #pragma unroll
   for (int t = 0; t < A; ++t) {
@@ -627,7 +645,7 @@ __device__ __forceinline__ void join_pieces(const A& a, const AttnLaunch& l, con
   // groups of pieces: one when all are joined directly, else about the root
   // of their number; group k has pieces k n / groups .. (k + 1) n / groups - 1
   int groups = 1, k = 0;
-  if (it.pieces > kJoinDirect) {
+  if (it.pieces > KindOf<A>::kJoinDirect) {
     while (groups * groups < it.pieces) ++groups;
     k = (int)((uint32_t)(it.piece * groups) / (uint32_t)it.pieces);
     if ((int)((uint32_t)((k + 1) * it.pieces) / (uint32_t)groups) <= it.piece) ++k;
@@ -646,7 +664,7 @@ __device__ __forceinline__ void join_pieces(const A& a, const AttnLaunch& l, con
     for (int d = wave; d < S::DT; d += WAVES) {
       float4v sum[TILES][1];
       float top[TILES], weight[TILES];
-      join_fragments<DIM, TILES, TILES, 1>(res, lane, 0, d, count, slot, sum, top, weight);
+      join_fragments<DIM, TILES, TILES, 1, KindOf<A>::at_once(TILES)>(res, lane, 0, d, count, slot, sum, top, weight);
       const int at = (l.slots + first / 2) * S::kBytes;
 #pragma unroll
       for (int rt = 0; rt < TILES; ++rt) {
@@ -689,7 +707,7 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention_join_kernel(A a, At
       if (rt * 16 >= rows_here) break;
       float4v sum[1][B];
       float top[1], weight[1];
-      join_fragments<DIM, TILES, 1, B>(partial_of(l), lane, rt, d0, it.pieces, [&](int i) { return it.first + i; }, sum,
+      join_fragments<DIM, TILES, 1, B, KindOf<A>::at_once(B)>(partial_of(l), lane, rt, d0, it.pieces, [&](int i) { return it.first + i; }, sum,
                                        top, weight);
       if (rt * 16 + c16 < rows_here) {
 #pragma unroll
@@ -701,10 +719,8 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention_join_kernel(A a, At
 }
 
 // Segments of a call whose requests all bring max_rows rows.
-template <typename A>
-int64_t most_segments(int requests, int max_rows, int q_heads, int heads, int dim) {
+int64_t most_segments(const Form& f, int requests, int max_rows, int q_heads, int heads) {
   const int64_t rows = (int64_t)max_rows * (q_heads / heads);
-  const Form f = form_for<A>(rows, dim);
   const int64_t tiles = (rows + f.rows() - 1) / f.rows();
   return (int64_t)requests * heads * (tiles < 1 ? 1 : tiles);
 }
@@ -732,9 +748,9 @@ hipError_t launch_kernel(Kernel kernel, int threads, size_t lds, const A& a, con
 
 template <typename A>
 size_t scratch_bytes_for(int requests, int max_rows, int q_heads, int heads, int dim, int table_width) {
-  const int64_t segments = most_segments<A>(requests, max_rows, q_heads, heads, dim);
+  const Form f = form_of<A>(requests, max_rows, q_heads, heads, dim, table_width);
+  const int64_t segments = most_segments(f, requests, max_rows, q_heads, heads);
   if (table_width <= kMinPiecePages || segments >= kMaxPieces) return kKvZeroedBytes;
-  const Form f = form_for<A>((int64_t)max_rows * (q_heads / heads), dim);
   const size_t slots = wanted_pieces(segments);
   return kKvZeroedBytes + (slots + slots / 2) * slot_bytes(f, dim);
 }
@@ -748,8 +764,8 @@ struct AttnPlan {
 template <typename A>
 AttnPlan plan_of(const A& a) {
   const int dim = a.cache.dim, group = a.q_heads / a.cache.heads;
-  const Form f = form_for<A>((int64_t)a.max_rows * group, dim);
-  const int64_t segments = most_segments<A>(a.requests, a.max_rows, a.q_heads, a.cache.heads, dim);
+  const Form f = form_of<A>(a.requests, a.max_rows, a.q_heads, a.cache.heads, dim, a.table_width);
+  const int64_t segments = most_segments(f, a.requests, a.max_rows, a.q_heads, a.cache.heads);
   AttnLaunch l;
   l.tile_rows = f.rows();
   l.group = group;

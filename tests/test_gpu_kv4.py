@@ -269,6 +269,32 @@ def test_attention_ragged_and_windows(kv, dim, hq, hk, window):
     c.check(c.run(window=window), window)
 
 
+# so many requests that the row tiles of a KV head stay together: two and three tiles, some pieces cut
+MANY = [(1 + (i * 5) % 8, 8 + (i * 397) % 1500) for i in range(19)] + [(8, 2600)]
+
+
+@pytest.mark.parametrize("dim,hq,hk", [(128, 15, 3), (64, 12, 3), (128, 16, 4), (64, 30, 6)])
+@pytest.mark.parametrize("window", [0, 1, 70, 1000])
+def test_attention_tiles_together(kv, dim, hq, hk, window):
+    c = AttnCase4(kv, MANY, hq, hk, dim, 16)
+    clean = c.run(window=window)
+    c.check(clean, window)
+    # NaN in the unseen, and a value group that only later rows of the last request see
+    used = np.zeros(c.codes.shape[1:4], bool)
+    for r, (n, t) in enumerate(c.lens):
+        for j in range(max(0, t - n + 1 - window) if window else 0, t):
+            used[c.table[r, j // PAGE], :, j % PAGE] = True
+    c.scale[:, ~used] = 0x7F
+    assert np.array_equal(c.run(window=window), clean)
+    c.scale[1, c.table[-1, 2595 // PAGE], 1, 2595 % PAGE, 2] = 0x7F
+    y = c.run(window=window)
+    group, hit = hq // hk, np.zeros(y.shape, bool)
+    hit[-5:, group:2 * group, 32:48] = True
+    if window == 1:
+        hit[-4:] = False
+    assert np.array_equal(np.isnan(y), hit) and np.array_equal(y[~hit], clean[~hit])
+
+
 @pytest.mark.parametrize("window", [0, 77])
 def test_attention_ragged_many_rows(kv, window):
     c = AttnCase4(kv, [(70, 300), (1, 1), (0, 40), (200, 210), (33, 64), (100, 1300)], 6, 2, 128, 15)
