@@ -10,13 +10,14 @@
 // the rest, which is what the log of a likely token is made of) and sum of x exp(x).
 //
 // The likeliest tokens.  Keys, unique and in the order wanted: the logit's bits made
-// ascending, then the index descending.  A wavefront holds a list of at most `top` keys in
-// LDS and its smallest one as a bound.  Of a tile, only lanes whose largest logit is among
-// the `top` largest of all lanes' (found by bisection with ballots: the scalar unit's
-// work) or above the bound can hold one that counts; these are put behind the list, which
-// is then cut to its `top` largest by a bisection over the keys.  Wavefronts of a
-// workgroup and then the pieces of a row are joined in the same way, by the last one of a row
-// to arrive, which also sorts.
+// ascending, then the index descending.  A wavefront holds a list of keys in LDS and the
+// least value that can still count.  Of a tile, only lanes whose largest logit reaches it
+// can hold one; when more than `top` lanes do, the value that `top` of them reach is the
+// new least one (found by bisection with ballots: the scalar unit's work).  What
+// reaches it goes behind the list, which is cut to its `top` largest keys, by
+// bisections of the values and then of the indices of the last one's equals, when it is
+// long and at the end.  Wavefronts of a workgroup and then the pieces of a row are
+// joined in the same way, by the last one of a row to arrive, which also sorts.
 #include "qpn_common.h"
 #include "qpn_kv_internal.h"
 
@@ -24,76 +25,96 @@ namespace qpn {
 
 namespace {
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 16;
 constexpr int kThreads = kWaves * kLanes;
 constexpr int kVecs = 2;                          // loads of eight logits a lane, of a tile
 constexpr int kTile = kVecs * 8 * kLanes;         // tokens of a wavefront's tile
 constexpr int kMaxTop = kLogprobsMaxTop;
+constexpr int kListMax = 192;                     // keys that a list is cut behind
+constexpr int kListRoom = kListMax + kLanes;
 constexpr int kMaxPieces = 64;                    // of a row
-constexpr int kWanted = 1024;                     // workgroups wanted
+constexpr int kWanted = 256;                      // workgroups wanted: one a CU
 constexpr int kCounterStep = 16;                  // 32-bit words between the rows' counters
 static_assert((size_t)kWanted * kCounterStep * 4 <= kKvZeroedBytes, "a counter per row of a call with cut rows");
 constexpr float kLowest = -65504.0f;
+constexpr uint32_t kOrderedLowest = 0x03FFu;      // ordered(-inf)
 
 struct Sums {
   float m;      // the largest logit (at least kLowest)
   double s, u;  // sum exp(x), sum of x exp(x), x in units of log 2, against m
 };
 
-// What a piece leaves in scratch, and behind it its kMaxTop keys.
+// What a piece leaves in scratch; its keys, `top` of them, lie behind those of all rows.
 struct Piece {
   double s, u;
   float m, pad;
-  uint64_t keys[kMaxTop];
 };
 
 // Ascending in the value: the bits of an FP16 number (no NaN; -0 as 0).
-__device__ __forceinline__ uint32_t ordered(float z) {
-  const uint32_t b = __builtin_bit_cast(uint16_t, (_Float16)(z + 0.0f));
+__device__ __forceinline__ uint32_t ordered_bits(uint32_t b) {
+  b = b == 0x8000u ? 0u : b;
   return b & 0x8000u ? b ^ 0xFFFFu : b | 0x8000u;
+}
+__device__ __forceinline__ uint32_t ordered(float z) {
+  return ordered_bits(__builtin_bit_cast(uint16_t, (_Float16)z));
 }
 __device__ __forceinline__ float value_of(uint32_t o) {
   return (float)__builtin_bit_cast(_Float16, (uint16_t)(o & 0x8000u ? o ^ 0x8000u : o ^ 0xFFFFu));
 }
-__device__ __forceinline__ uint64_t key_of(float z, int64_t index) {
-  return (uint64_t)ordered(z) << 32 | (uint32_t)(0xFFFFFFFFu - (uint32_t)index);
+__device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) {
+  return (uint64_t)order << 32 | (0xFFFFFFFFu - index);
 }
 __device__ __forceinline__ int index_of(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
-// The largest t for which at least `top` of the wavefront's values are t or more (0 when
-// there are fewer values).
-__device__ __forceinline__ uint32_t bound_of(uint32_t x, int top) {
+// The largest t of `bits` bits for which at least `top` of the wavefront's values (N a lane;
+// those of lanes without one: 0) are t or more, and how many are; 0 and their number when
+// there are fewer.
+template <int N>
+__device__ __forceinline__ uint32_t bound_of(const uint32_t (&x)[N], int bits, int top, int& reach) {
   uint32_t t = 0;
+  reach = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) reach += __popcll(__ballot(x[i] != 0));
 #pragma unroll 1
-  for (int bit = 15; bit >= 0; --bit) {
+  for (int bit = bits - 1; bit >= 0 && reach != top; --bit) {
     const uint32_t up = t | 1u << bit;
-    const int n = __popcll(__ballot(x >= up));
-    if (n >= top) t = up;
-    if (n == top) break;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += __popcll(__ballot(x[i] >= up));
+    if (n >= top) t = up, reach = n;
   }
   return t;
 }
-// The same of up to N keys a lane (0: none).
+
+// The `top` largest of the wavefront's keys (N a lane; 0: none, and there are more than `top`):
+// true at those.
 template <int N>
-__device__ __forceinline__ uint64_t bound_of(const uint64_t (&key)[N], int top) {
-  uint64_t t = 0;
-#pragma unroll 1
-  for (int bit = 47; bit >= 0; --bit) {
-    const uint64_t up = t | 1ull << bit;
-    int n = 0;
+__device__ __forceinline__ void choose(const uint64_t (&key)[N], int top, bool (&in)[N]) {
+  uint32_t value[N];
+  int reach;
 #pragma unroll
-    for (int i = 0; i < N; ++i) n += __popcll(__ballot(key[i] >= up));
-    if (n >= top) t = up;
-    if (n == top) break;
+  for (int i = 0; i < N; ++i) value[i] = (uint32_t)(key[i] >> 32);
+  const uint32_t t = bound_of(value, 16, top, reach);
+#pragma unroll
+  for (int i = 0; i < N; ++i) in[i] = key[i] != 0 && value[i] >= t;
+  if (reach == top) return;
+  // of those equal to the last value the lowest indices (the others' keys count as their largest)
+  int above = 0;
+  uint32_t equal[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    above += __popcll(__ballot(value[i] > t));
+    equal[i] = key[i] != 0 && value[i] == t ? (uint32_t)key[i] & 0xFFFFFFu : 0u;
   }
-  return t;
+  const uint32_t least = bound_of(equal, 24, top - above, reach);
+#pragma unroll
+  for (int i = 0; i < N; ++i) in[i] = key[i] != 0 && (value[i] > t || (value[i] == t && equal[i] >= least));
 }
 
 // A wavefront's list.
 struct List {
-  uint64_t* keys;  // LDS, room for kMaxTop + kTile
+  uint64_t* keys;  // LDS, kListRoom of them
   int count;       // uniform
-  uint64_t bound;  // the smallest key when there are `top`, else 0
 
   // Puts the keys of the lanes in `mask` behind the list.
   __device__ __forceinline__ void add(uint64_t mask, uint64_t key) {
@@ -102,62 +123,87 @@ struct List {
     count += __popcll(mask);
   }
 
-  // Cuts the list to its `top` largest keys.  N keys a lane at a time: what is above
-  // the bound of those and of the ones before.
-  __device__ __forceinline__ void cut(int top) {
-    constexpr int N = 4;
-    const int lane = threadIdx.x & 63;
-    if (count <= top) return;
-    int kept = 0;
-#pragma unroll 1
-    for (int from = 0; from < count; from += (N - 1) * kLanes) {
-      uint64_t key[N];
-      key[0] = lane < kept ? keys[lane] : 0;  // (top is at most 64)
+  // The `top` largest of N keys a lane (0: none) are the list.
+  template <int N>
+  __device__ __forceinline__ void take(const uint64_t (&key)[N], int all, int top) {
+    bool in[N];
+    if (all > top) {
+      choose(key, top, in);
+    } else {
 #pragma unroll
-      for (int i = 1; i < N; ++i) {
-        const int at = from + (i - 1) * kLanes + lane;
-        key[i] = at >= kept && at < count ? keys[at] : 0;
-      }
-      bound = bound_of(key, top);
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before they are written over
-      const int all = count;
-      count = 0;
-#pragma unroll
-      for (int i = 0; i < N; ++i) add(__ballot(key[i] >= bound && key[i] != 0), key[i]);
-      kept = count;
-      count = all;
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      for (int i = 0; i < N; ++i) in[i] = key[i] != 0;
     }
-    count = kept;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what is written over has been read
+    count = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) add(__ballot(in[i]), key[i]);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  }
+
+  __device__ __forceinline__ void cut(int top) {
+    constexpr int N = kListRoom / kLanes;
+    const int lane = threadIdx.x & 63;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what was added is there
+    if (count <= top) return;
+    uint64_t key[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) key[i] = i * kLanes + lane < count ? keys[i * kLanes + lane] : 0;
+    take(key, count, top);
   }
 };
 
+// x of another lane by a data-parallel move, and a reduction by them: within 16 lanes (quad_perm
+// 1 0 3 2 and 2 3 0 1, mirrored within 8 and 16), then between the four rows.
+template <int CTRL>
+__device__ __forceinline__ float moved(float x) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double moved(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xF, 0xF, false);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  x = fmaxf(x, moved<0xB1>(x));
+  x = fmaxf(x, moved<0x4E>(x));
+  x = fmaxf(x, moved<0x141>(x));
+  x = fmaxf(x, moved<0x140>(x));
+  x = fmaxf(x, __shfl_xor(x, 16));
+  return fmaxf(x, __shfl_xor(x, 32));
+}
+__device__ __forceinline__ double wave_sum(double x) {
+  x += moved<0xB1>(x);
+  x += moved<0x4E>(x);
+  x += moved<0x141>(x);
+  x += moved<0x140>(x);
+  x += __shfl_xor(x, 16);
+  return x + __shfl_xor(x, 32);
+}
+
 // The sums of the wavefront's lanes, in every lane.  (A logit of +inf leaves NaN in s.)
-__device__ __forceinline__ Sums wave_joined(const Sums& x, double c) {
+__device__ __forceinline__ Sums wave_joined(const Sums& x, float c) {
   Sums r;
-  r.m = x.m;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) r.m = fmaxf(r.m, __shfl_xor(r.m, d));
-  const double d0 = ((double)x.m - (double)r.m) * c, f = exp2(d0);
-  r.s = x.s * f;
-  r.u = (x.u + x.s * d0) * f;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) r.s += __shfl_xor(r.s, d), r.u += __shfl_xor(r.u, d);
+  r.m = wave_max(x.m);
+  const float d = (x.m - r.m) * c;
+  const double f = (double)__builtin_amdgcn_exp2f(d);
+  r.s = wave_sum(x.s * f);
+  r.u = wave_sum((x.u + x.s * (double)fmaxf(d, -1e4f)) * f);
   return r;
 }
 
 template <bool TOP>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int pieces) {
-  __shared__ uint64_t s_keys[TOP ? kWaves : 1][TOP ? kMaxTop + kTile : 1];
+  __shared__ uint64_t s_keys[TOP ? kWaves : 1][TOP ? kListRoom : 1];
   __shared__ Sums s_sums[kWaves];
   __shared__ int s_count[kWaves];
-  __shared__ uint32_t s_arrival;
+  __shared__ uint32_t s_least, s_arrival;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int row = (int)(blockIdx.x / (uint32_t)pieces), piece = (int)(blockIdx.x % (uint32_t)pieces);
   const uint16_t* const z = a.logits + row * a.logits_stride;
   // (as good as any larger one: two logits differ by 2^-24 at least)
-  const double cd = fmin(a.inv_temperature, 1e30) * 1.4426950408889634074;
-  const float c = (float)cd;
+  const float c = (float)(fmin(a.inv_temperature, 1e30) * 1.4426950408889634074);
 
   // tiles start at multiples of 16 bytes: the first one up to seven tokens before the row
   const int before = (int)(((uintptr_t)z >> 1) & 7);
@@ -178,9 +224,18 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
   };
 
   Sums mine{kLowest, 0.0, 0.0};
-  List list{s_keys[TOP ? wave : 0], 0, 0};
+  List list{s_keys[TOP ? wave : 0], 0};
+  // the least value that counts (ordered): that `top` tokens reach, whichever wavefront saw them
+  uint32_t least = kOrderedLowest;
   half8 next[kVecs];
   if (first + wave < end) load(first + wave, next);
+  const int32_t token = a.tokens[row];
+  const bool good_token = token >= 0 && token < a.n;
+  const uint16_t token_logit = z[good_token ? token : 0];
+  if constexpr (TOP) {
+    if (threadIdx.x == 0) s_least = kOrderedLowest;
+    __syncthreads();
+  }
 #pragma unroll 1
   for (int64_t tile = first + wave; tile < end; tile += kWaves) {
     half8 x[kVecs];
@@ -203,44 +258,74 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
       s += (double)e;
       u = __builtin_fmaf(e, fmaxf(t, -1e4f), u);  // (0 where the logit is -inf)
     }
-    mine.u = (mine.u + mine.s * (double)up) * f + (double)u;
+    mine.u = (mine.u + mine.s * (double)fmaxf(up, -1e4f)) * f + (double)u;
     mine.s = s;
     mine.m = m;
     if constexpr (TOP) {
-      const uint32_t o = ordered(high), floor = (uint32_t)(list.bound >> 32);
-      if (__ballot(o >= floor)) {
-        const float least = value_of(max(bound_of(o, a.top), max(floor, 0x03FFu)));
-#pragma unroll
-        for (int i = 0; i < kVecs * 8; ++i) {
-          uint64_t mask = __ballot(zf[i] >= least);
-          if (mask) {
-            const int64_t at = tile * kTile - before + (i >> 3) * (8 * kLanes) + lane * 8 + (i & 7);
-            const uint64_t key = key_of(zf[i], at);
-            mask = __ballot(zf[i] >= least && at >= 0 && at < a.n && key > list.bound);
-            list.add(mask, key);
+      least = max(least, (uint32_t)__builtin_amdgcn_readfirstlane((int)*(volatile uint32_t*)&s_least));
+      float at_least = value_of(least);
+      const int lanes = __popcll(__ballot(high >= at_least));
+      if (lanes > 0) {
+        if (lanes > a.top) {
+          int reach;
+          const uint32_t o[1] = {ordered(high)};
+          const uint32_t t = bound_of(o, 16, a.top, reach);
+          if (t > least) {
+            least = t;
+            at_least = value_of(least);
+            if (lane == 0) atomicMax(&s_least, least);
           }
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        list.cut(a.top);
+        uint32_t bits = 0;  // of the tokens that count
+#pragma unroll
+        for (int i = 0; i < kVecs * 8; ++i) bits |= (uint32_t)(zf[i] >= at_least) << i;
+        const int64_t from = tile * kTile - before + lane * 8;
+        if (tile * kTile < before || (tile + 1) * kTile - before > a.n) {  // not the ones that are not there
+#pragma unroll
+          for (int i = 0; i < kVecs * 8; ++i) {
+            const int64_t at = from + (i >> 3) * (8 * kLanes) + (i & 7);
+            if (at < 0 || at >= a.n) bits &= ~(1u << i);
+          }
+        }
+        while (__ballot(bits != 0)) {  // one of each lane
+          const bool some = bits != 0;
+          const int i = some ? __ffs((int)bits) - 1 : 0;
+          bits &= bits - 1;
+          uint32_t w = 0;
+#pragma unroll
+          for (int d = 0; d < kVecs * 4; ++d) {
+            const u32x4 y = __builtin_bit_cast(u32x4, x[d >> 2]);
+            w = d == i >> 1 ? y[d & 3] : w;
+          }
+          const uint32_t o = ordered_bits(i & 1 ? w >> 16 : w & 0xFFFFu);
+          list.add(__ballot(some), key_of(o, (uint32_t)(from + (i >> 3) * (8 * kLanes) + (i & 7))));
+          if (list.count > kListMax) list.cut(a.top);
+        }
       }
     }
   }
+  if constexpr (TOP) list.cut(a.top);
 
   // the workgroup's wavefronts, by the first one
-  mine = wave_joined(mine, cd);
+  mine = wave_joined(mine, c);
   if (lane == 0) s_sums[wave] = mine, s_count[wave] = list.count;
   __syncthreads();
   Piece* const out = reinterpret_cast<Piece*>((uint8_t*)a.scratch + kKvZeroedBytes) + (int64_t)row * pieces;
+  uint64_t* const out_keys = reinterpret_cast<uint64_t*>((uint8_t*)a.scratch + kKvZeroedBytes +
+                                                         (int64_t)a.rows * pieces * sizeof(Piece)) + (int64_t)row * pieces * a.top;
   if (wave == 0) {
-    mine = wave_joined(lane < kWaves ? s_sums[lane] : Sums{kLowest, 0.0, 0.0}, cd);
+    mine = wave_joined(lane < kWaves ? s_sums[lane] : Sums{kLowest, 0.0, 0.0}, c);
     if constexpr (TOP) {
-#pragma unroll 1
-      for (int w = 1; w < kWaves; ++w) {
-        const int n = s_count[w];  // (at most top <= 64)
-        list.add(n >= 64 ? ~0ull : (1ull << n) - 1, s_keys[w][lane < n ? lane : 0]);
+      constexpr int N = kWaves * kMaxTop / kLanes, PER = kLanes / kMaxTop;  // lists that a step reads
+      uint64_t key[N];
+      int all = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int w = i * PER + lane / kMaxTop;
+        key[i] = lane % kMaxTop < s_count[w] ? s_keys[w][lane % kMaxTop] : 0;
+        all += __popcll(__ballot(key[i] != 0));
       }
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      list.cut(a.top);
+      list.take(key, all, a.top);
     }
     if (pieces > 1) {
       if (lane == 0) {
@@ -249,73 +334,77 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
         __hip_atomic_store(&out[piece].m, mine.m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
       if (TOP && lane < a.top)
-        __hip_atomic_store(&out[piece].keys[lane], lane < list.count ? list.keys[lane] : 0ull, __ATOMIC_RELAXED,
+        __hip_atomic_store(&out_keys[piece * a.top + lane], lane < list.count ? list.keys[lane] : 0ull, __ATOMIC_RELAXED,
                            __HIP_MEMORY_SCOPE_AGENT);
     }
   }
+  if (wave != 0) return;  // (no barrier follows)
   if (pieces > 1) {
     uint32_t* const counter = (uint32_t*)a.scratch + row * kCounterStep;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wavefront's stores are there
-    __syncthreads();
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
       const uint32_t arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       if (arrived == (uint32_t)(pieces - 1))
         __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       s_arrival = arrived;
     }
-    __syncthreads();
-    if (s_arrival != (uint32_t)(pieces - 1)) return;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    if (__builtin_amdgcn_readfirstlane((int)*(volatile uint32_t*)&s_arrival) != pieces - 1) return;
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-  }
-  if (wave != 0) return;
-  if (pieces > 1) {
     Sums of{kLowest, 0.0, 0.0};
+    constexpr int N = 8;  // keys a lane, of a step
+    const int total = TOP ? pieces * a.top : 0;
+    uint64_t key[N + 1];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int at = i * kLanes + lane;
+      key[i] = at < total ? __hip_atomic_load(&out_keys[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+    }
     if (lane < pieces) {
       of.s = __hip_atomic_load(&out[lane].s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       of.u = __hip_atomic_load(&out[lane].u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       of.m = __hip_atomic_load(&out[lane].m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    mine = wave_joined(of, cd);
+    mine = wave_joined(of, c);
     if constexpr (TOP) {
-      // all pieces' keys through the list, as many as it has room for at a time
-      list.count = 0;
-      list.bound = 0;
-      const int total = pieces * a.top;
-#pragma unroll 1
-      for (int from = 0; from < total; from += kTile) {
-#pragma unroll 1
-        for (int i = from; i < total && i < from + kTile; i += kLanes) {
-          const int at = i + lane;
-          uint64_t key = 0;
-          if (at < total && at < from + kTile)
-            key = __hip_atomic_load(&out[at / a.top].keys[at % a.top], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-          list.add(__ballot(key > list.bound), key);
+      key[N] = 0;
+      for (int from = 0;;) {
+        int all = 0;
+#pragma unroll
+        for (int i = 0; i <= N; ++i) all += __popcll(__ballot(key[i] != 0));
+        list.take(key, all, a.top);
+        from += N * kLanes;
+        if (from >= total) break;
+        key[N] = lane < list.count ? list.keys[lane] : 0;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const int at = from + i * kLanes + lane;
+          key[i] = at < total ? __hip_atomic_load(&out_keys[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
         }
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        list.cut(a.top);
       }
     }
   }
 
-  const double log2e = 1.4426950408889634074;
   const bool bad = !(mine.s > 0.0) || !(mine.s < __builtin_inf()) || !(mine.m < __builtin_inff());
-  const double rest = mine.s - 1.0;                       // what is not the largest token
-  const double log_s = bad ? __builtin_nan("") : log1p(rest);
+  const double log_s = bad ? __builtin_nan("") : log1p(mine.s - 1.0);  // (what is not the largest token)
   if (lane == 0) {
-    const int32_t token = a.tokens[row];
     double lp = __builtin_nan("");
-    if (token >= 0 && token < a.n && !bad)
-      lp = ((double)(float)__builtin_bit_cast(_Float16, z[token]) - (double)mine.m) * a.inv_temperature - log_s;
+    if (good_token && !bad)
+      lp = ((double)(float)__builtin_bit_cast(_Float16, token_logit) - (double)mine.m) * a.inv_temperature - log_s;
     a.logprob[row] = (float)lp;
-    a.entropy[row] = (float)(log_s - mine.u / mine.s / log2e);
+    a.entropy[row] = (float)(log_s - mine.u / mine.s * 0.69314718055994530942);
   }
   if constexpr (TOP) {
     // by rank: the keys are all different
     const uint64_t key = lane < list.count ? list.keys[lane] : 0;
     int rank = 0;
 #pragma unroll 1
-    for (int i = 0; i < list.count; ++i) rank += list.keys[i] > key;
-    if (lane >= list.count) rank = lane;  // (never: there are top tokens, unless some are NaN)
+    for (int i = 0; i < list.count; ++i) {
+      const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), i) << 32 |
+                             (uint32_t)__builtin_amdgcn_readlane((int)key, i);
+      rank += other > key;
+    }
+    if (lane >= list.count) rank = lane;  // (only where logits are NaN: there are top tokens else)
     if (lane < a.top) {
       const bool none = bad || lane >= list.count;
       const double zi = value_of((uint32_t)(key >> 32));
@@ -339,7 +428,7 @@ int pieces_of(int rows, int64_t n) {
 
 size_t logprobs_scratch_bytes(int rows, int64_t n) {
   const int p = pieces_of(rows, n);
-  return kKvZeroedBytes + (p > 1 ? (size_t)rows * p * sizeof(Piece) : 0);
+  return kKvZeroedBytes + (p > 1 ? (size_t)rows * p * (sizeof(Piece) + kMaxTop * sizeof(uint64_t)) : 0);
 }
 
 hipError_t launch_logprobs(const LogprobsArgs& a) {
