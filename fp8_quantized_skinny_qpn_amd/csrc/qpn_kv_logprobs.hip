@@ -5,9 +5,10 @@
 //   log p_i = x_i - log S,   entropy = log S - sum x_i exp(x_i) / S.
 //
 // One pass.  A row is cut into pieces, one workgroup each, a piece into tiles of 1024
-// tokens that the workgroup's wavefronts take in turn, 16 tokens a lane.  Each lane
-// keeps its own running maximum, S (in 64 bits: the largest token's 1 must not swallow
-// the rest, which is what the log of a likely token is made of) and sum of x exp(x).
+// tokens that the workgroup's wavefronts take in turn, 16 tokens a lane.  A wavefront
+// has a running maximum (at first the largest of all the workgroup's first tiles), each lane
+// its part of S (in 64 bits: the largest token's 1 must not swallow the rest, which is what
+// the log of a likely token is made of) and of the sum of x exp(x).
 //
 // The likeliest tokens.  Keys, unique and in the order wanted: the logit's bits made
 // ascending, then the index descending.  A wavefront holds a list of keys in LDS and the
@@ -104,9 +105,9 @@ __device__ __forceinline__ void choose(const uint64_t (&key)[N], int top, bool (
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     above += __popcll(__ballot(value[i] > t));
-    equal[i] = key[i] != 0 && value[i] == t ? (uint32_t)key[i] & 0xFFFFFFu : 0u;
+    equal[i] = key[i] != 0 && value[i] == t ? ((uint32_t)key[i] & 0xFFFFFFu) + 1 : 0u;
   }
-  const uint32_t least = bound_of(equal, 24, top - above, reach);
+  const uint32_t least = bound_of(equal, 25, top - above, reach);
 #pragma unroll
   for (int i = 0; i < N; ++i) in[i] = key[i] != 0 && (value[i] > t || (value[i] == t && equal[i] >= least));
 }
@@ -182,6 +183,13 @@ __device__ __forceinline__ double wave_sum(double x) {
   return x + __shfl_xor(x, 32);
 }
 
+__device__ __forceinline__ float lane_max(const half8 (&x)[kVecs]) {
+  float high = -__builtin_inff();
+#pragma unroll
+  for (int i = 0; i < kVecs * 8; ++i) high = fmaxf(high, (float)x[i >> 3][i & 7]);
+  return high;
+}
+
 // The sums of the wavefront's lanes, in every lane.  (A logit of +inf leaves NaN in s.)
 __device__ __forceinline__ Sums wave_joined(const Sums& x, float c) {
   Sums r;
@@ -198,7 +206,8 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
   __shared__ uint64_t s_keys[TOP ? kWaves : 1][TOP ? kListRoom : 1];
   __shared__ Sums s_sums[kWaves];
   __shared__ int s_count[kWaves];
-  __shared__ uint32_t s_least, s_arrival;
+  __shared__ uint32_t s_least, s_arrival, s_first_value[kWaves];
+  __shared__ float s_first_max[kWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int row = (int)(blockIdx.x / (uint32_t)pieces), piece = (int)(blockIdx.x % (uint32_t)pieces);
   const uint16_t* const z = a.logits + row * a.logits_stride;
@@ -223,18 +232,37 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
     }
   };
 
-  Sums mine{kLowest, 0.0, 0.0};
-  List list{s_keys[TOP ? wave : 0], 0};
-  // the least value that counts (ordered): that `top` tokens reach, whichever wavefront saw them
-  uint32_t least = kOrderedLowest;
   half8 next[kVecs];
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) next[v] = half8{} - (_Float16)__builtin_inff();
   if (first + wave < end) load(first + wave, next);
   const int32_t token = a.tokens[row];
   const bool good_token = token >= 0 && token < a.n;
   const uint16_t token_logit = z[good_token ? token : 0];
-  if constexpr (TOP) {
-    if (threadIdx.x == 0) s_least = kOrderedLowest;
+
+  // what the wavefronts' first tiles tell: the largest logit, and a value that `top` tokens
+  // reach, since each wavefront has its share of them
+  {
+    const float high = lane_max(next), m = wave_max(high);
+    if (lane == 0) s_first_max[wave] = m;
+    if constexpr (TOP) {
+      int reach;
+      const uint32_t o[1] = {ordered(high)};
+      const uint32_t v = bound_of(o, 16, (a.top + kWaves - 1) / kWaves, reach);
+      if (lane == 0) s_first_value[wave] = v;
+      if (threadIdx.x == 0) s_least = kOrderedLowest;
+    }
     __syncthreads();
+  }
+  Sums mine{fmaxf(wave_max(lane < kWaves ? s_first_max[lane] : kLowest), kLowest), 0.0, 0.0};
+  List list{s_keys[TOP ? wave : 0], 0};
+  // the least value that counts (ordered): that `top` tokens reach, whichever wavefront saw them
+  uint32_t least = kOrderedLowest;
+  if constexpr (TOP) {
+    uint32_t v = lane < kWaves ? s_first_value[lane] : 0xFFFFu;
+#pragma unroll
+    for (int d = 1; d < kWaves; d <<= 1) v = min(v, (uint32_t)__shfl_xor((int)v, d));
+    least = max(least, (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
   }
 #pragma unroll 1
   for (int64_t tile = first + wave; tile < end; tile += kWaves) {
@@ -242,25 +270,33 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) x[v] = next[v];
     if (tile + kWaves < end) load(tile + kWaves, next);
-    float zf[kVecs * 8], high = -__builtin_inff();
-#pragma unroll
-    for (int i = 0; i < kVecs * 8; ++i) {
-      zf[i] = (float)x[i >> 3][i & 7];
-      high = fmaxf(high, zf[i]);
+    const float high = lane_max(x);
+    if (__ballot(high > mine.m)) {
+      const float m = wave_max(fmaxf(high, mine.m)), d = (mine.m - m) * c;
+      const double f = (double)__builtin_amdgcn_exp2f(d);
+      mine.u = (mine.u + mine.s * (double)fmaxf(d, -1e4f)) * f;
+      mine.s *= f;
+      mine.m = m;
     }
-    const float m = fmaxf(mine.m, high), up = (mine.m - m) * c;
-    const double f = (double)__builtin_amdgcn_exp2f(up);
-    double s = mine.s * f;
     float u = 0.0f;
+    if (__ballot(high == mine.m)) {  // the largest one's 1 is not added to small numbers in 32 bits
 #pragma unroll
-    for (int i = 0; i < kVecs * 8; ++i) {
-      const float t = (zf[i] - m) * c, e = __builtin_amdgcn_exp2f(t);
-      s += (double)e;
-      u = __builtin_fmaf(e, fmaxf(t, -1e4f), u);  // (0 where the logit is -inf)
+      for (int i = 0; i < kVecs * 8; ++i) {
+        const float t = ((float)x[i >> 3][i & 7] - mine.m) * c, e = __builtin_amdgcn_exp2f(t);
+        mine.s += (double)e;
+        u = __builtin_fmaf(e, fmaxf(t, -1e4f), u);  // (0 where the logit is -inf)
+      }
+    } else {
+      float s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kVecs * 8; ++i) {
+        const float t = ((float)x[i >> 3][i & 7] - mine.m) * c, e = __builtin_amdgcn_exp2f(t);
+        s += e;
+        u = __builtin_fmaf(e, fmaxf(t, -1e4f), u);
+      }
+      mine.s += (double)s;
     }
-    mine.u = (mine.u + mine.s * (double)fmaxf(up, -1e4f)) * f + (double)u;
-    mine.s = s;
-    mine.m = m;
+    mine.u += (double)u;
     if constexpr (TOP) {
       least = max(least, (uint32_t)__builtin_amdgcn_readfirstlane((int)*(volatile uint32_t*)&s_least));
       float at_least = value_of(least);
@@ -276,29 +312,43 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
             if (lane == 0) atomicMax(&s_least, least);
           }
         }
-        uint32_t bits = 0;  // of the tokens that count
+        // the tokens that count: bit 8 + d for the lower half of the lane's word d, 24 + d for
+        // the upper one, the signs of their differences from the least value
+        uint32_t bits = 0;
+        uint32_t less = __builtin_bit_cast(uint16_t, (_Float16)at_least) ^ 0x8000u;
+        less = less == 0x8000u ? 0u : less;  // (+0 for 0, so that -0 is no less)
+        const half2v from2 = __builtin_bit_cast(half2v, less * 0x10001u);
 #pragma unroll
-        for (int i = 0; i < kVecs * 8; ++i) bits |= (uint32_t)(zf[i] >= at_least) << i;
-        const int64_t from = tile * kTile - before + lane * 8;
-        if (tile * kTile < before || (tile + 1) * kTile - before > a.n) {  // not the ones that are not there
+        for (int d = 0; d < kVecs * 4; ++d) {
+          const u32x4 w = __builtin_bit_cast(u32x4, x[d >> 2]);
+          const uint32_t y = w[d & 3];
+          const half2v diff = __builtin_bit_cast(half2v, y) + from2;
+          bits = bits >> 1 | (~__builtin_bit_cast(uint32_t, diff) & 0x80008000u);
+        }
+        if (least == kOrderedLowest) bits = 0xFF00FF00u;  // (-inf less -inf has no sign)
+        // but for those that are not there, before the row or behind it
+        const int64_t tile_at = tile * kTile - before;
+        if (tile_at < 0 || tile_at + kTile > a.n) {
+          int l = lane * 8;
+          asm volatile("; ends" : "+v"(l));
 #pragma unroll
           for (int i = 0; i < kVecs * 8; ++i) {
-            const int64_t at = from + (i >> 3) * (8 * kLanes) + (i & 7);
-            if (at < 0 || at >= a.n) bits &= ~(1u << i);
+            const int64_t at = tile_at + l + (i >> 3) * (8 * kLanes) + (i & 7);
+            if (at < 0 || at >= a.n) bits &= ~(1u << (8 + (i >> 1) + 16 * (i & 1)));
           }
         }
         while (__ballot(bits != 0)) {  // one of each lane
           const bool some = bits != 0;
-          const int i = some ? __ffs((int)bits) - 1 : 0;
+          const int b = some ? __ffs((int)bits) - 1 : 8, d = b & 7;
           bits &= bits - 1;
           uint32_t w = 0;
 #pragma unroll
-          for (int d = 0; d < kVecs * 4; ++d) {
-            const u32x4 y = __builtin_bit_cast(u32x4, x[d >> 2]);
-            w = d == i >> 1 ? y[d & 3] : w;
+          for (int k = 0; k < kVecs * 4; ++k) {
+            const u32x4 y = __builtin_bit_cast(u32x4, x[k >> 2]);
+            w = k == d ? y[k & 3] : w;
           }
-          const uint32_t o = ordered_bits(i & 1 ? w >> 16 : w & 0xFFFFu);
-          list.add(__ballot(some), key_of(o, (uint32_t)(from + (i >> 3) * (8 * kLanes) + (i & 7))));
+          const uint32_t o = ordered_bits(b & 16 ? w >> 16 : w & 0xFFFFu);
+          list.add(__ballot(some), key_of(o, (uint32_t)tile_at + lane * 8 + (d >> 2) * (8 * kLanes) + 2 * (d & 3) + (b >> 4)));
           if (list.count > kListMax) list.cut(a.top);
         }
       }
