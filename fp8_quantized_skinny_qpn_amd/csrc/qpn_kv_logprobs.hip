@@ -98,7 +98,7 @@ __device__ __forceinline__ void choose(const uint64_t (&key)[N], int top, bool (
   const uint32_t t = bound_of(value, 16, top, reach);
 #pragma unroll
   for (int i = 0; i < N; ++i) in[i] = key[i] != 0 && value[i] >= t;
-  if (reach == top) return;
+  if (reach <= top) return;
   // of those equal to the last value the lowest indices (the others' keys count as their largest)
   int above = 0;
   uint32_t equal[N];
@@ -124,34 +124,56 @@ struct List {
     count += __popcll(mask);
   }
 
-  // The `top` largest of N keys a lane (0: none) are the list.
-  template <int N>
-  __device__ __forceinline__ void take(const uint64_t (&key)[N], int all, int top) {
+  // Cuts the list to its `top` largest keys.
+  __device__ __forceinline__ void cut(int top) {
+    constexpr int N = kListRoom / kLanes;
+    const int lane = threadIdx.x & 63;
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what was added is there
+    uint64_t key[N];
     bool in[N];
-    if (all > top) {
-      choose(key, top, in);
-    } else {
 #pragma unroll
-      for (int i = 0; i < N; ++i) in[i] = key[i] != 0;
-    }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what is written over has been read
+    for (int i = 0; i < N; ++i) key[i] = i * kLanes + lane < count ? keys[i * kLanes + lane] : 0;
+    choose(key, top, in);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // read before they are written over
     count = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) add(__ballot(in[i]), key[i]);
     asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   }
-
-  __device__ __forceinline__ void cut(int top) {
-    constexpr int N = kListRoom / kLanes;
-    const int lane = threadIdx.x & 63;
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // what was added is there
-    if (count <= top) return;
-    uint64_t key[N];
-#pragma unroll
-    for (int i = 0; i < N; ++i) key[i] = i * kLanes + lane < count ? keys[i * kLanes + lane] : 0;
-    take(key, count, top);
-  }
 };
+
+// Of the wavefront's keys (N a lane; 0: none) a key a lane, the `top` largest among them.
+// room: LDS for kLanes keys.
+template <int N>
+__device__ __forceinline__ uint64_t gathered(const uint64_t (&key)[N], int top, uint64_t* room) {
+  uint32_t value[N];
+  bool in[N];
+  int reach;
+#pragma unroll
+  for (int i = 0; i < N; ++i) value[i] = (uint32_t)(key[i] >> 32);
+  const uint32_t t = bound_of(value, 16, top, reach);
+#pragma unroll
+  for (int i = 0; i < N; ++i) in[i] = key[i] != 0 && value[i] >= t;
+  if (reach > kLanes) choose(key, top, in);  // (many equal ones)
+  List list{room, 0};
+#pragma unroll
+  for (int i = 0; i < N; ++i) list.add(__ballot(in[i]), key[i]);
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  const int lane = threadIdx.x & 63;
+  return lane < list.count ? room[lane] : 0;
+}
+
+// A key's place among the wavefront's, the largest first (they are all different; 0: none).
+__device__ __forceinline__ int rank_of(uint64_t key) {
+  int rank = 0;
+  for (uint64_t left = __ballot(key != 0); left; left &= left - 1) {
+    const int i = __ffsll((unsigned long long)left) - 1;
+    const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), i) << 32 |
+                           (uint32_t)__builtin_amdgcn_readlane((int)key, i);
+    rank += other > key;
+  }
+  return rank;
+}
 
 // x of another lane by a data-parallel move, and a reduction by them: within 16 lanes (quad_perm
 // 1 0 3 2 and 2 3 0 1, mirrored within 8 and 16), then between the four rows.
@@ -205,8 +227,9 @@ template <bool TOP>
 __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int pieces) {
   __shared__ uint64_t s_keys[TOP ? kWaves : 1][TOP ? kListRoom : 1];
   __shared__ Sums s_sums[kWaves];
-  __shared__ int s_count[kWaves];
-  __shared__ uint32_t s_least, s_arrival, s_first_value[kWaves];
+  __shared__ uint64_t s_all[TOP ? kWaves * kMaxTop : 1];
+  __shared__ int s_total;
+  __shared__ uint32_t s_least, s_first_value[kWaves];
   __shared__ float s_first_max[kWaves];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int row = (int)(blockIdx.x / (uint32_t)pieces), piece = (int)(blockIdx.x % (uint32_t)pieces);
@@ -250,7 +273,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
       const uint32_t o[1] = {ordered(high)};
       const uint32_t v = bound_of(o, 16, (a.top + kWaves - 1) / kWaves, reach);
       if (lane == 0) s_first_value[wave] = v;
-      if (threadIdx.x == 0) s_least = kOrderedLowest;
+      if (threadIdx.x == 0) s_least = kOrderedLowest, s_total = 0;
     }
     __syncthreads();
   }
@@ -354,62 +377,70 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
       }
     }
   }
-  if constexpr (TOP) list.cut(a.top);
 
   // the workgroup's wavefronts, by the first one
   mine = wave_joined(mine, c);
-  if (lane == 0) s_sums[wave] = mine, s_count[wave] = list.count;
+  if (lane == 0) s_sums[wave] = mine;
+  if constexpr (TOP) {  // (in any order: the keys are all different)
+    if (list.count > kMaxTop) list.cut(a.top);
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&s_total, list.count);
+    at = __builtin_amdgcn_readfirstlane(at);
+    if (lane < list.count) s_all[at + lane] = list.keys[lane];
+  }
   __syncthreads();
-  Piece* const out = reinterpret_cast<Piece*>((uint8_t*)a.scratch + kKvZeroedBytes) + (int64_t)row * pieces;
-  uint64_t* const out_keys = reinterpret_cast<uint64_t*>((uint8_t*)a.scratch + kKvZeroedBytes +
-                                                         (int64_t)a.rows * pieces * sizeof(Piece)) + (int64_t)row * pieces * a.top;
-  if (wave == 0) {
-    mine = wave_joined(lane < kWaves ? s_sums[lane] : Sums{kLowest, 0.0, 0.0}, c);
-    if constexpr (TOP) {
-      constexpr int N = kWaves * kMaxTop / kLanes, PER = kLanes / kMaxTop;  // lists that a step reads
-      uint64_t key[N];
-      int all = 0;
+  if (wave != 0) return;  // (no barrier follows)
+  mine = wave_joined(lane < kWaves ? s_sums[lane] : Sums{kLowest, 0.0, 0.0}, c);
+  uint64_t key = 0;  // the likeliest tokens', a lane each
+  if constexpr (TOP) {
+    const int total = s_total;
+    if (total <= kLanes) {
+      key = lane < total ? s_all[lane] : 0;
+    } else {
+      constexpr int N = kWaves * kMaxTop / kLanes;
+      uint64_t some[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const int w = i * PER + lane / kMaxTop;
-        key[i] = lane % kMaxTop < s_count[w] ? s_keys[w][lane % kMaxTop] : 0;
-        all += __popcll(__ballot(key[i] != 0));
-      }
-      list.take(key, all, a.top);
-    }
-    if (pieces > 1) {
-      if (lane == 0) {
-        __hip_atomic_store(&out[piece].s, mine.s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(&out[piece].u, mine.u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        __hip_atomic_store(&out[piece].m, mine.m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      if (TOP && lane < a.top)
-        __hip_atomic_store(&out_keys[piece * a.top + lane], lane < list.count ? list.keys[lane] : 0ull, __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
+      for (int i = 0; i < N; ++i) some[i] = i * kLanes + lane < total ? s_all[i * kLanes + lane] : 0;
+      key = gathered(some, a.top, list.keys);
     }
   }
-  if (wave != 0) return;  // (no barrier follows)
   if (pieces > 1) {
+    Piece* const out = reinterpret_cast<Piece*>((uint8_t*)a.scratch + kKvZeroedBytes) + (int64_t)row * pieces;
+    uint64_t* const out_keys = reinterpret_cast<uint64_t*>((uint8_t*)a.scratch + kKvZeroedBytes +
+                                                           (int64_t)a.rows * pieces * sizeof(Piece)) + (int64_t)row * pieces * a.top;
+    if (lane == 0) {
+      __hip_atomic_store(&out[piece].s, mine.s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&out[piece].u, mine.u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      __hip_atomic_store(&out[piece].m, mine.m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if constexpr (TOP) {  // `top` of them, and zeros where there are fewer
+      const int rank = key ? rank_of(key) : lane;
+      if (rank < a.top)
+        __hip_atomic_store(&out_keys[piece * a.top + rank], key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
     uint32_t* const counter = (uint32_t*)a.scratch + row * kCounterStep;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wavefront's stores are there
+    uint32_t arrived = 0;
     if (lane == 0) {
-      const uint32_t arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      arrived = __hip_atomic_fetch_add(counter, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       if (arrived == (uint32_t)(pieces - 1))
         __hip_atomic_store(counter, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      s_arrival = arrived;
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    if (__builtin_amdgcn_readfirstlane((int)*(volatile uint32_t*)&s_arrival) != pieces - 1) return;
+    if (__builtin_amdgcn_readfirstlane((int)arrived) != pieces - 1) return;
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
     Sums of{kLowest, 0.0, 0.0};
-    constexpr int N = 8;  // keys a lane, of a step
+    constexpr int N = 4;  // keys a lane, of a step
     const int total = TOP ? pieces * a.top : 0;
-    uint64_t key[N + 1];
+    uint64_t some[N + 1];
+    const auto load_keys = [&](int from) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int at = i * kLanes + lane;
-      key[i] = at < total ? __hip_atomic_load(&out_keys[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-    }
+      for (int i = 0; i < N; ++i) {
+        const int at = from + i * kLanes + lane;
+        some[i] = at < total ? __hip_atomic_load(&out_keys[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
+      }
+    };
+    if constexpr (TOP) load_keys(0);
     if (lane < pieces) {
       of.s = __hip_atomic_load(&out[lane].s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       of.u = __hip_atomic_load(&out[lane].u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -417,20 +448,13 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
     }
     mine = wave_joined(of, c);
     if constexpr (TOP) {
-      key[N] = 0;
+      key = 0;
       for (int from = 0;;) {
-        int all = 0;
-#pragma unroll
-        for (int i = 0; i <= N; ++i) all += __popcll(__ballot(key[i] != 0));
-        list.take(key, all, a.top);
+        some[N] = key;
+        key = gathered(some, a.top, list.keys);
         from += N * kLanes;
         if (from >= total) break;
-        key[N] = lane < list.count ? list.keys[lane] : 0;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          const int at = from + i * kLanes + lane;
-          key[i] = at < total ? __hip_atomic_load(&out_keys[at], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0;
-        }
+        load_keys(from);
       }
     }
   }
@@ -445,18 +469,11 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
     a.entropy[row] = (float)(log_s - mine.u / mine.s * 0.69314718055994530942);
   }
   if constexpr (TOP) {
-    // by rank: the keys are all different
-    const uint64_t key = lane < list.count ? list.keys[lane] : 0;
-    int rank = 0;
-#pragma unroll 1
-    for (int i = 0; i < list.count; ++i) {
-      const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), i) << 32 |
-                             (uint32_t)__builtin_amdgcn_readlane((int)key, i);
-      rank += other > key;
-    }
-    if (lane >= list.count) rank = lane;  // (only where logits are NaN: there are top tokens else)
-    if (lane < a.top) {
-      const bool none = bad || lane >= list.count;
+    const int found = __popcll(__ballot(key != 0));
+    // (there are `top` of them, unless some logits are NaN; then the lanes behind fill the row)
+    const int rank = key ? rank_of(key) : lane;
+    if (rank < a.top && (key || lane >= found)) {
+      const bool none = bad || !key;
       const double zi = value_of((uint32_t)(key >> 32));
       a.top_ids[(int64_t)row * a.top + rank] = none ? -1 : index_of(key);
       a.top_logprobs[(int64_t)row * a.top + rank] =
