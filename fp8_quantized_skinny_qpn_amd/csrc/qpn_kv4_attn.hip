@@ -261,7 +261,7 @@ template <int DIM, int RT>
 __global__ __launch_bounds__(kFewWaves * 64) void attention4_few_kernel(Attention4Args a, AttnLaunch l) {
   using S = Slot<DIM, RT>;
   using L = FewLds<DIM, RT>;
-  constexpr int W = L::W, KS = L::KS, ROWS = L::ROWS, DT = L::DT, G = DIM / 64;
+  constexpr int W = L::W, KS = L::KS, ROWS = L::ROWS, DT = L::DT;
   __shared__ uint32_t s_arrival;
   extern __shared__ __attribute__((aligned(16))) uint8_t s_few[];
   L& s = *reinterpret_cast<L*>(s_few);
@@ -514,26 +514,21 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention4_many_kernel(Attent
     const auto has = [&](int j) { return j * kManyWaves + wave < 2 * LOADS; };
     const auto is_key = [&](int j) { return j * kManyWaves + wave < LOADS; };
     const auto number = [&](int j) { return (j * kManyWaves + wave) % LOADS; };
+    // The same instructions for both: a branch between them would end in moves of what is loaded,
+    // and so in a wait for it.
+    constexpr int WORDS = G == 1 ? 2 : G;  // of scales: of keys the first, of values (G > 1) one a group
     u32x4 held[MINE];
-    uint32_t scale[MINE][4];
+    uint32_t scale[MINE][WORDS];
     const auto fetch = [&](int j, int64_t at) {
-      if (!has(j)) return;
-      const int n = number(j);
+      if constexpr (2 * LOADS % kManyWaves != 0)
+        if (!has(j)) return;
+      const int n = number(j), step = is_key(j) ? 0 : G == 1 ? 4 : 256;
       held[j] = *reinterpret_cast<const u32x4*>((is_key(j) ? a.cache.k : a.cache.v) + at * kv4_codes(DIM) + n * 1024 + lane * 16);
-      if (is_key(j)) {  // bytes 2 n, 2 n + 1 of the lane's 4 G
-        scale[j][0] = *reinterpret_cast<const uint16_t*>(a.cache.k_scale + at * kv4_scales(DIM) + lane * (4 * G) + 2 * n);
-      } else {          // the tokens of the load: 16 / LOADS of each group
-        const uint8_t* from = a.cache.v_scale + at * kv4_scales(DIM) + (lane >> 2) * 16 + n * (16 / LOADS);
-        if constexpr (G == 1) {
-          const u32x2 s = *reinterpret_cast<const u32x2*>(from);
-          scale[j][0] = s[0], scale[j][1] = s[1];
-        } else {
+      // of keys bytes 2 n, 2 n + 1 of the lane's 4 G; of values the tokens of the load, 16 / LOADS of each group
+      const uint8_t* const from = (is_key(j) ? a.cache.k_scale : a.cache.v_scale) + at * kv4_scales(DIM);
+      const uint32_t in_lane = is_key(j) ? lane * (4 * G) + (2 * n & ~3) : (lane >> 2) * 16 + (n * (16 / LOADS) & ~3);
 #pragma unroll
-          for (int i = 0; i < G; ++i)
-            scale[j][i] = G == 2 ? *reinterpret_cast<const uint32_t*>(from + i * 256)
-                                 : *reinterpret_cast<const uint16_t*>(from + i * 256);
-        }
-      }
+      for (int i = 0; i < WORDS; ++i) scale[j][i] = *reinterpret_cast<const uint32_t*>(from + step * i + in_lane);
     };
     // Codes to operands.  Values of a page that some rows of the tile see only a part of:
     // NaN scales become zeros, and a flag is left.
@@ -542,7 +537,7 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention4_many_kernel(Attent
       const int n = number(j), base = page * kKvPage;
       const u32x4 x = held[j];
       if (is_key(j)) {
-        const half2v sc = scale_pair(scale[j][0], 0);
+        const half2v sc = scale_pair(n % 2 ? scale[j][0] >> 16 : scale[j][0], 0);
 #pragma unroll
         for (int u = 0; u < 2; ++u) {  // the group n' = 2 n + u = t G + i
           const int at = 2 * n + u, t = at / G, i = at % G;
@@ -551,10 +546,14 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention4_many_kernel(Attent
         }
         return;
       }
+      if constexpr (G == 4) {  // two of a word's four
+#pragma unroll
+        for (int i = 0; i < G; ++i) scale[j][i] = n % 2 ? scale[j][i] >> 16 : scale[j][i] & 0xFFFFu;
+      }
       if (base + kKvPage > all.lim_min || base < all.low_max) {
         uint32_t any = 0;
 #pragma unroll
-        for (int i = 0; i < (G == 1 ? 2 : G); ++i) {
+        for (int i = 0; i < WORDS; ++i) {
           const uint32_t bad = nan_bytes(scale[j][i]) >> 7;
           any |= bad;
           scale[j][i] &= ~(bad * 255u);

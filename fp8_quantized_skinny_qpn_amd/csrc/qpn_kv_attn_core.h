@@ -491,12 +491,6 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset
                : "memory", "m0");
 }
 
-// The same with 4 bytes a lane, lane i's to lds + 4 i.
-__device__ __forceinline__ void word_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"(uniform((int)lds)), "v"(offset), "s"(base)
-               : "memory", "m0");
-}
-
 template <int RT, typename A>
 __device__ __forceinline__ View<RT> view_of(const A& a, const AttnLaunch& l, const Req& q, int lane,
                                             int first, int rows) {
