@@ -470,7 +470,7 @@ struct ManyLds {
 
 template <int DIM, int RT>
 __global__ __launch_bounds__(kManyWaves * 64) void attention4_many_kernel(Attention4Args a, AttnLaunch l) {
-  using R = Rows<DIM, RT>;
+  using R = Rows<DIM, RT, true>;
   using S = Slot<DIM, RT * kManyWaves>;
   constexpr int DT = R::DT, KS = R::KS, ROWS = 16 * RT * kManyWaves, G = DIM / 64;
   constexpr int LOADS = DIM / 32;                                    // 1 KiB of codes each, of the keys or the values
@@ -503,6 +503,7 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention4_many_kernel(Attent
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) load_query<DIM>(a, l, q, it.head, lane, row_first, rows_here, rt, qr[rt]);
     const float factor = unit_of(a.cache.k_unit, it.head) * (a.scale * 1.44269504088896340736f);
+    const float kc = fminf(fmaxf(factor, 0x1p-126f), 0x1p127f);  // (as above)
     const float v_unit = unit_of(a.cache.v_unit, it.head);
     if (threadIdx.x == 0) lds.nan = 0;
     lds_barrier();
@@ -611,14 +612,12 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention4_many_kernel(Attent
     };
     // step `page`: the weights and values of `page`, the scores of page + 1; keys of page + 2
     // and values of page + 1 become operands
-    const auto fetch_all = [&](int page, int at) {  // keys of `page`, values of the one before
-      const int64_t keys_at = block_of(a, it.head, id_of(page, at));
-      const int64_t values_at = block_of(a, it.head, id_of(max(page - 1, lo), at));
-#pragma unroll
-      for (int j = 0; j < MINE; ++j) fetch(j, is_key(j) ? keys_at : values_at);
-    };
+    int id = 0, id1 = 0, id2 = 0;  // of `page`, page + 1, page + 2
+    int64_t at1 = 0, at2 = 0;      // where the last two are
     if (lo < hi) {
-      fetch_all(lo, 0);
+      id2 = id_of(lo, 0), at2 = block_of(a, it.head, id2);
+#pragma unroll
+      for (int j = 0; j < MINE; ++j) fetch(j, at2);
 #pragma unroll
       for (int j = 0; j < MINE; ++j)
         if (is_key(j)) put(j, lo);
@@ -629,21 +628,33 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention4_many_kernel(Attent
       if (at > 0 && (at & 63) == 0) now = next;
       if ((at & 63) == 32 && lo + (at | 63) + 1 < hi) next = load_ids(a, table, q.bad, lane, lo + (at | 63) + 1, 1, hi);
       lds_barrier();  // values of this page and keys of the next are in LDS, the other buffers have been read
-      if (lo < hi) fetch_all(page + 2, at);
+      if (lo < hi) {
+        id = id1, id1 = id2, at1 = at2;
+        id2 = id_of(page + 2, at), at2 = block_of(a, it.head, id2);
+#pragma unroll
+        for (int j = 0; j < MINE; ++j) fetch(j, is_key(j) ? at2 : at1);
+      }
       const auto key = [&](int i) { return lds.k[(page + 1) & 1][i][lane]; };
-      const float next_kc = id_of(page + 1, at) < 0 ? __builtin_nanf("") : factor;
       if (page >= my_lo && page < my_hi) {
         const int base = page * kKvPage;
+        if (__builtin_expect(id < 0 || factor != factor, 0)) {  // no page, or no unit: NaN to the rows that see it
+#pragma unroll
+          for (int t = 0; t < 4; ++t)
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) s[t][rt] *= __builtin_nanf("");
+        }
         if (base + kKvPage > see.lim_min || base < see.low_max) {
           mask_page<RT>(s, base, g, see);
 #pragma unroll
           for (int rt = 0; rt < RT; ++rt) high[rt] = page_max<RT>(s, rt);
         }
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) high[rt] *= kc;
         rows.raise(high);
         half8 p[2][RT];
         float4v ahead[4][RT];  // (of a page that is not there: of what the buffer holds, and not used)
-        rows.weigh(s, 0.0f, 1.0f, p, key, qr, ahead);
-        rows.accumulate([&](int i) { return lds.v[page & 1][i][lane]; }, p, ahead, next_kc, high);
+        rows.weigh(s, kc, 1.0f, p, key, qr, ahead);
+        rows.accumulate([&](int i) { return lds.v[page & 1][i][lane]; }, p, ahead, 1.0f, high);
 #pragma unroll
         for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -651,11 +662,7 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention4_many_kernel(Attent
       } else if (page + 1 == my_lo && my_lo < my_hi) {
         R::scores(key, qr, s);
 #pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-#pragma unroll
-          for (int t = 0; t < 4; ++t) s[t][rt] *= next_kc;
-          high[rt] = page_max<RT>(s, rt);
-        }
+        for (int rt = 0; rt < RT; ++rt) high[rt] = page_max<RT>(s, rt);
       }
       if (lo < hi) {
 #pragma unroll
@@ -678,8 +685,7 @@ __global__ __launch_bounds__(kManyWaves * 64) void attention4_many_kernel(Attent
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       if (rt * 16 >= rows_here) break;
-      float weight = rows.sum[rt] + __shfl_xor(rows.sum[rt], 16);
-      weight += __shfl_xor(weight, 32);
+      const float weight = rows.sum[rt][0];
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
         const float4v sum = rows.o[d][rt] * v_unit;

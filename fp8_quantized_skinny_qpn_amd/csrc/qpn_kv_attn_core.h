@@ -10,6 +10,8 @@
 // order (of more than kJoinDirect pieces: in groups, then the groups).
 #pragma once
 
+#include <type_traits>
+
 #include "qpn_common.h"
 #include "qpn_kv_internal.h"
 
@@ -306,12 +308,17 @@ __device__ __forceinline__ float page_max(const float4v (&s)[4][RT], int rt) {
   return mx;
 }
 
-// The rows of a wavefront and their running sums.
-template <int DIM, int RT>
+// The rows of a wavefront and their running sums.  ONE: one positive factor makes all
+// scores exponents, and values have no page scales.  Then the factor is in the exponentials'
+// fused multiply-add, and the matrix unit sums the FP16 weights (32 tokens under one operand
+// of ones), where the scales of the 8-bit pages take a multiplication of each score and an
+// FP32 sum of what the FP16 weights are rounded from.
+template <int DIM, int RT, bool ONE = false>
 struct Rows {
   static constexpr int KS = DIM / 32;  // k-steps of the scores
   static constexpr int DT = DIM / 16;  // tiles of output dimensions
-  float m[RT], sum[RT];
+  float m[RT];
+  std::conditional_t<ONE, float4v, float> sum[RT];  // (of a float4v all four alike, of all lanes' tokens)
   float4v o[DT][RT];
   float vref;  // what the sums are in units of: a power of two
 
@@ -325,7 +332,7 @@ struct Rows {
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       m[t] = kLowest;
-      sum[t] = 0.0f;
+      sum[t] = {};
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[d][t] = float4v{0, 0, 0, 0};
     }
@@ -396,7 +403,8 @@ struct Rows {
   // The weights of a page's scores s, as the B operands of the second product
   // (p[h]: tokens of tiles 2 h and 2 h + 1), times vs / vref, 1 to kScaleSlack:
   // exp2(score - m + lift), lift = log2(vs / vref), with their FP32 sum times
-  // vref / vs (drop) added to the sums; and the scores of the next page.  The
+  // vref / vs (drop) added to the sums; and the scores of the next page.  (ONE:
+  // exp2(score lift - m), and no sums.)  The
   // two in turn, operand by operand, so that the vector and the matrix unit
   // work at the same time: left to itself the compiler puts one behind the other.
   template <typename Key>
@@ -408,7 +416,7 @@ struct Rows {
     float off[RT], part[RT][2];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      off[rt] = lift - m[rt];
+      off[rt] = ONE ? -m[rt] : lift - m[rt];
       part[rt][0] = part[rt][1] = 0.0f;
     }
 #pragma unroll
@@ -424,18 +432,19 @@ struct Rows {
 #pragma unroll
       for (int v = i * 16 * RT / N; v < (i + 1) * 16 * RT / N; ++v) {
         const int rt = v / 16, t = v / 4 % 4, r = v % 4;
-        const float x = __builtin_amdgcn_exp2f(s[t][rt][r] + off[rt]);
-        part[rt][r & 1] += x;
+        const float x = __builtin_amdgcn_exp2f(ONE ? __builtin_fmaf(s[t][rt][r], lift, off[rt]) : s[t][rt][r] + off[rt]);
+        if constexpr (!ONE) part[rt][r & 1] += x;
         s[t][rt][r] = x;
         if (v % 8 == 7) p[t >> 1][rt] = to_half8(s[t - 1][rt], s[t][rt]);
-        if (v % 16 == 15) sum[rt] = __builtin_fmaf(part[rt][0] + part[rt][1], drop, sum[rt]);
+        if constexpr (!ONE)
+          if (v % 16 == 15) sum[rt] = __builtin_fmaf(part[rt][0] + part[rt][1], drop, sum[rt]);
       }
       __builtin_amdgcn_sched_barrier(0);
     }
   }
 
-  // O^T += V^T P^T; and the next page's scores get their factor kc, and their
-  // largest is found.  value(i): the
+  // O^T += V^T P^T (ONE: and the sums of the weights); and the next page's scores get
+  // their factor kc (ONE: none), and their largest is found.  value(i): the
   // operand of dimension 16 (i / 2) + c16, tokens 16 t + 4 g + r of the tiles
   // t = 2 (i % 2) and one more.
   template <typename Value>
@@ -444,6 +453,13 @@ struct Rows {
     half8 vf[AHEAD + 1];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) vf[i] = value(i);
+    if constexpr (ONE) {
+      const half8 ones = {1, 1, 1, 1, 1, 1, 1, 1};
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) sum[rt] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, p[h][rt], sum[rt], 0, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (i + AHEAD < N) vf[(i + AHEAD) % (AHEAD + 1)] = value(i + AHEAD);
@@ -453,7 +469,7 @@ struct Rows {
 #pragma unroll
       for (int v = i * 8 * RT / N; v < (i + 1) * 8 * RT / N; ++v) {  // a pair of scores at a time
         const int rt = v / 8, t = v / 2 % 4, r = v % 2 * 2;
-        next[t][rt][r] *= kc, next[t][rt][r + 1] *= kc;
+        if constexpr (!ONE) next[t][rt][r] *= kc, next[t][rt][r + 1] *= kc;
         high[rt] = v % 8 ? fmaxf(fmaxf(high[rt], next[t][rt][r]), next[t][rt][r + 1]) : fmaxf(next[t][rt][r], next[t][rt][r + 1]);
       }
       __builtin_amdgcn_sched_barrier(0);
