@@ -75,6 +75,29 @@ __device__ __forceinline__ Codes quantise(const double x[8], double unit) {
   return {codes, scale};
 }
 
+// Whether a row behind `row` has its slot: 16 slots a lane at a time, in loads that do not wait
+// for one another.
+__device__ __forceinline__ bool taken_later(const int32_t* slots, int rows, int row, int32_t slot, int lane) {
+  constexpr int STEP = 4 * kLanes;
+  int from = row + 1;
+  bool later = false;
+  for (; rows - from >= 4 * STEP; from += 4 * STEP) {
+    int32_t s[4][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) __builtin_memcpy(s[i], slots + from + i * STEP + lane * 4, 16);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) later |= s[i >> 2][i & 3] == slot;
+    if (__ballot(later)) return true;
+  }
+  if (from >= rows) return false;
+  int32_t s[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s[i] = slots[min(from + i * kLanes + lane, rows - 1)];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) later |= s[i] == slot && from + i * kLanes + lane < rows;
+  return __ballot(later) != 0;
+}
+
 template <int DIM>
 __device__ __forceinline__ void append_tokens(const RopeAppend4Args& a, int wg, int waves_per_row) {
   constexpr int LPH = DIM / 8, HPW = kLanes / LPH;
@@ -91,9 +114,7 @@ __device__ __forceinline__ void append_tokens(const RopeAppend4Args& a, int wg, 
   Lane<DIM> f;
   f.load(a, lane_at, a.k_weight);
   const double k_unit = a.cache.k_unit[there ? head : 0], v_unit = a.cache.v_unit[there ? head : 0];
-  bool later = false;
-  for (int t = row + 1 + lane; t < a.rows; t += kLanes) later |= a.slots[t] == slot;
-  if (__ballot(later)) return;
+  if (taken_later(a.slots, a.rows, row, slot, lane)) return;
 
   double x[8];
   Rotor<double, DIM> rotor;

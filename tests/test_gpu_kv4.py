@@ -126,6 +126,17 @@ def test_append_slots_in_any_order(kv):
     append_case(kv, 128, 2, 1, slots, np.arange(502), 5, 7)
 
 
+@pytest.mark.parametrize("rows", [2, 63, 1025, 2300])
+def test_append_a_slot_taken_again(kv, rows):
+    rng = np.random.default_rng(rows)
+    slots = rng.permutation(40 * PAGE)[:rows].astype(np.int32)
+    first = rng.permutation(rows - 1)[:rows // 3 + 1]
+    for i in first:                                  # at any distance, also more than once
+        slots[rng.integers(i + 1, rows)] = slots[i]
+    slots[-1] = slots[0]
+    append_case(kv, 64, 2, 1, slots, rng.integers(0, 5000, rows), 40, rows)
+
+
 @pytest.mark.parametrize("unit", [2.0 ** -30, 2.0 ** -6, 0.7, 3.0e-3, 1000.0, 1e30])
 def test_append_units(kv, unit):
     # values far above what the unit holds (they saturate), of its size, far below (coarse scales, zeros), no power of two
