@@ -10,6 +10,8 @@ Tolerances, derived before the first run:
                            + tokens 2^-25 max |v| (weights below FP16's normal range, the largest being
                            at least 1) + 2^-25.
 """
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -606,3 +608,63 @@ def test_a_round_from_a_graph(kv, dim, hq, hk, rows):
     at = np.arange(total - rows, total)
     for got, want in zip(eager[-1][2:4], (k, v)):
         assert np.array_equal(host(got).astype(np.float64), want[table[0, at // PAGE], :, at % PAGE].reshape(rows, -1))
+
+
+def test_calls_beside_each_other(kv):
+    # attention and log probabilities whose sums pass through scratch: threads on one stream, other streams, graphs
+    c = AttnCase4(kv, [(8, 5000), (3, 900)], 10, 2, 128, 17)
+    ref = c.run()
+    c.check(ref)
+    cache, args = c.device(), (i32(c.row_start), i32(c.seq), i32(c.table), 8)
+    q = dev(c.q.reshape(11, -1))
+    rng = np.random.default_rng(18)
+    z, tokens = dev((3 * rng.standard_normal((4, 100001))).astype(np.float16)), i32(rng.integers(0, 100001, 4))
+    assert kv.attention4_scratch_bytes(2, 8, 10, 2, 128, c.width) > kv.SCRATCH_ZEROED
+    assert kv.logprobs_scratch_bytes(4, 100001) > kv.SCRATCH_ZEROED
+    want = [host(t) for t in (kv.attention(cache, q, *args), *kv.logprobs(z, tokens, 7))]
+    torch.cuda.synchronize()
+
+    def both(stream=None):
+        return [kv.attention(cache, q, *args, stream=stream), *kv.logprobs(z, tokens, 7, stream=stream)]
+
+    def same(got):
+        for g, w in zip(got, want):
+            assert np.array_equal(host(g), w)
+    one, others = torch.cuda.Stream(), [torch.cuda.Stream() for _ in range(3)]
+    got = [[] for _ in range(4)]
+
+    def work(i):
+        got[i] += [both(one) for _ in range(8)]
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert [len(g) for g in got] == [8] * 4
+    for g in got:
+        for outs in g:
+            same(outs)
+    log("streams")
+    outs = [both(s) for _ in range(4) for s in others]
+    torch.cuda.synchronize()
+    for o in outs:
+        same(o)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=one):
+            graphs.append((g, both() + both()))
+    for rep in range(4):
+        log(f"two graphs beside calls, {rep}")
+        for _, out in graphs:
+            for t in out:
+                t.zero_()
+        torch.cuda.synchronize()
+        for (g, _), s in zip(graphs, others):
+            with torch.cuda.stream(s):
+                g.replay()
+        eager = both(one)
+        torch.cuda.synchronize()
+        for out in (eager, *(o[i:i + 5] for _, o in graphs for i in (0, 5))):
+            same(out)
