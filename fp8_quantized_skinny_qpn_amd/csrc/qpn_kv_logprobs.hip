@@ -19,6 +19,8 @@
 // bisections of the values and then of the indices of the last one's equals, when it is
 // long and at the end.  Wavefronts of a workgroup and then the pieces of a row are
 // joined in the same way, by the last one of a row to arrive, which also sorts.
+#include <type_traits>
+
 #include "qpn_common.h"
 #include "qpn_kv_internal.h"
 
@@ -67,18 +69,71 @@ __device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) {
 }
 __device__ __forceinline__ int index_of(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
-// The largest t of `bits` bits for which at least `top` of the wavefront's values (N a lane;
-// those of lanes without one: 0) are t or more, and how many are; 0 and their number when
-// there are fewer.
+// x of another lane by a data-parallel move, and reductions by them: within 16 lanes (quad_perm
+// 1 0 3 2 and 2 3 0 1, mirrored within 8 and 16), then of the four rows' first lanes.  The
+// result is uniform.
+template <int CTRL, typename T>
+__device__ __forceinline__ T moved(T x) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
+}
+template <int CTRL>
+__device__ __forceinline__ double moved(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, false);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xF, 0xF, false);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+template <typename T>
+__device__ __forceinline__ T of_lane(T x, int lane) {
+  return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+}
+__device__ __forceinline__ double of_lane(double x, int lane) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)b, lane);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(b >> 32), lane);
+  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
+}
+template <typename T, typename Op>
+__device__ __forceinline__ T wave_reduced(T x, Op op) {
+  x = op(x, moved<0xB1>(x));
+  x = op(x, moved<0x4E>(x));
+  x = op(x, moved<0x141>(x));
+  x = op(x, moved<0x140>(x));
+  return op(op(of_lane(x, 0), of_lane(x, 16)), op(of_lane(x, 32), of_lane(x, 48)));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  return wave_reduced(x, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t x) {
+  return wave_reduced(x, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ uint32_t wave_min(uint32_t x) {
+  return wave_reduced(x, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+__device__ __forceinline__ double wave_sum(double x) {
+  return wave_reduced(x, [](double a, double b) { return a + b; });
+}
+
+// The largest t for which at least `top` of the wavefront's values (N a lane; those of lanes
+// without one: 0) are t or more, and how many are; 0 and their number when there are fewer.
+// Bisected between the least and the largest of them.
 template <int N>
-__device__ __forceinline__ uint32_t bound_of(const uint32_t (&x)[N], int bits, int top, int& reach) {
-  uint32_t t = 0;
+__device__ __forceinline__ uint32_t bound_of(const uint32_t (&x)[N], int top, int& reach) {
+  uint32_t low = 0xFFFFFFFFu, high = 0;
   reach = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i) reach += __popcll(__ballot(x[i] != 0));
+  for (int i = 0; i < N; ++i) {
+    reach += __popcll(__ballot(x[i] != 0));
+    high = max(high, x[i]);
+    low = min(low, x[i] - 1u);  // (0: the largest)
+  }
+  if (reach < top) return 0;
+  if (reach == 0) return 0;
+  uint32_t t = wave_min(low) + 1;
+  const uint32_t most = wave_max(high);
 #pragma unroll 1
-  for (int bit = bits - 1; bit >= 0 && reach != top; --bit) {
-    const uint32_t up = t | 1u << bit;
+  for (int bit = 31 - __clz((int)(most - t)); bit >= 0 && reach != top; --bit) {
+    const uint32_t up = t + (1u << bit);
     int n = 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) n += __popcll(__ballot(x[i] >= up));
@@ -95,7 +150,7 @@ __device__ __forceinline__ void choose(const uint64_t (&key)[N], int top, bool (
   int reach;
 #pragma unroll
   for (int i = 0; i < N; ++i) value[i] = (uint32_t)(key[i] >> 32);
-  const uint32_t t = bound_of(value, 16, top, reach);
+  const uint32_t t = bound_of(value, top, reach);
 #pragma unroll
   for (int i = 0; i < N; ++i) in[i] = key[i] != 0 && value[i] >= t;
   if (reach <= top) return;
@@ -107,7 +162,7 @@ __device__ __forceinline__ void choose(const uint64_t (&key)[N], int top, bool (
     above += __popcll(__ballot(value[i] > t));
     equal[i] = key[i] != 0 && value[i] == t ? ((uint32_t)key[i] & 0xFFFFFFu) + 1 : 0u;
   }
-  const uint32_t least = bound_of(equal, 25, top - above, reach);
+  const uint32_t least = bound_of(equal, top - above, reach);
 #pragma unroll
   for (int i = 0; i < N; ++i) in[i] = key[i] != 0 && (value[i] > t || (value[i] == t && equal[i] >= least));
 }
@@ -151,7 +206,7 @@ __device__ __forceinline__ uint64_t gathered(const uint64_t (&key)[N], int top, 
   int reach;
 #pragma unroll
   for (int i = 0; i < N; ++i) value[i] = (uint32_t)(key[i] >> 32);
-  const uint32_t t = bound_of(value, 16, top, reach);
+  const uint32_t t = bound_of(value, top, reach);
 #pragma unroll
   for (int i = 0; i < N; ++i) in[i] = key[i] != 0 && value[i] >= t;
   if (reach > kLanes) choose(key, top, in);  // (many equal ones)
@@ -173,36 +228,6 @@ __device__ __forceinline__ int rank_of(uint64_t key) {
     rank += other > key;
   }
   return rank;
-}
-
-// x of another lane by a data-parallel move, and a reduction by them: within 16 lanes (quad_perm
-// 1 0 3 2 and 2 3 0 1, mirrored within 8 and 16), then between the four rows.
-template <int CTRL>
-__device__ __forceinline__ float moved(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
-}
-template <int CTRL>
-__device__ __forceinline__ double moved(double x) {
-  const uint64_t b = (uint64_t)__double_as_longlong(x);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xF, 0xF, false);
-  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
-}
-__device__ __forceinline__ float wave_max(float x) {
-  x = fmaxf(x, moved<0xB1>(x));
-  x = fmaxf(x, moved<0x4E>(x));
-  x = fmaxf(x, moved<0x141>(x));
-  x = fmaxf(x, moved<0x140>(x));
-  x = fmaxf(x, __shfl_xor(x, 16));
-  return fmaxf(x, __shfl_xor(x, 32));
-}
-__device__ __forceinline__ double wave_sum(double x) {
-  x += moved<0xB1>(x);
-  x += moved<0x4E>(x);
-  x += moved<0x141>(x);
-  x += moved<0x140>(x);
-  x += __shfl_xor(x, 16);
-  return x + __shfl_xor(x, 32);
 }
 
 __device__ __forceinline__ float lane_max(const half8 (&x)[kVecs]) {
@@ -269,10 +294,10 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
     const float high = lane_max(next), m = wave_max(high);
     if (lane == 0) s_first_max[wave] = m;
     if constexpr (TOP) {
-      int reach;
-      const uint32_t o[1] = {ordered(high)};
-      const uint32_t v = bound_of(o, 16, (a.top + kWaves - 1) / kWaves, reach);
-      if (lane == 0) s_first_value[wave] = v;
+      static_assert(kMaxTop <= 2 * kWaves, "its share is a token or two");
+      float v = m;
+      if (a.top > kWaves && __popcll(__ballot(high == m)) == 1) v = wave_max(high == m ? -__builtin_inff() : high);
+      if (lane == 0) s_first_value[wave] = ordered(v);
       if (threadIdx.x == 0) s_least = kOrderedLowest, s_total = 0;
     }
     __syncthreads();
@@ -282,10 +307,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
   // the least value that counts (ordered): that `top` tokens reach, whichever wavefront saw them
   uint32_t least = kOrderedLowest;
   if constexpr (TOP) {
-    uint32_t v = lane < kWaves ? s_first_value[lane] : 0xFFFFu;
-#pragma unroll
-    for (int d = 1; d < kWaves; d <<= 1) v = min(v, (uint32_t)__shfl_xor((int)v, d));
-    least = max(least, (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+    least = max(least, wave_min(lane < kWaves ? s_first_value[lane] : 0xFFFFu));
   }
 #pragma unroll 1
   for (int64_t tile = first + wave; tile < end; tile += kWaves) {
@@ -328,7 +350,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
         if (lanes > a.top) {
           int reach;
           const uint32_t o[1] = {ordered(high)};
-          const uint32_t t = bound_of(o, 16, a.top, reach);
+          const uint32_t t = bound_of(o, a.top, reach);
           if (t > least) {
             least = t;
             at_least = value_of(least);
@@ -398,11 +420,17 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
     if (total <= kLanes) {
       key = lane < total ? s_all[lane] : 0;
     } else {
-      constexpr int N = kWaves * kMaxTop / kLanes;
-      uint64_t some[N];
+      const auto gather = [&](auto n) {
+        constexpr int N = decltype(n)::value;
+        uint64_t some[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) some[i] = i * kLanes + lane < total ? s_all[i * kLanes + lane] : 0;
-      key = gathered(some, a.top, list.keys);
+        for (int i = 0; i < N; ++i) some[i] = i * kLanes + lane < total ? s_all[i * kLanes + lane] : 0;
+        key = gathered(some, a.top, list.keys);
+      };
+      if (total <= 2 * kLanes)
+        gather(std::integral_constant<int, 2>{});
+      else
+        gather(std::integral_constant<int, kWaves * kMaxTop / kLanes>{});
     }
   }
   if (pieces > 1) {
@@ -414,10 +442,16 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
       __hip_atomic_store(&out[piece].u, mine.u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       __hip_atomic_store(&out[piece].m, mine.m, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    if constexpr (TOP) {  // `top` of them, and zeros where there are fewer
-      const int rank = key ? rank_of(key) : lane;
-      if (rank < a.top)
-        __hip_atomic_store(&out_keys[piece * a.top + rank], key, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if constexpr (TOP) {  // `top` of them in any order, and zeros where there are fewer
+      const uint64_t one[1] = {key};
+      bool in[1] = {key != 0};
+      if (__popcll(__ballot(in[0])) > a.top) choose(one, a.top, in);
+      const uint64_t mask = __ballot(in[0]), other = ~mask;
+      const uint64_t mine_of = in[0] ? mask : other;
+      const int at = (in[0] ? 0 : __popcll(mask)) +
+                     __builtin_amdgcn_mbcnt_hi((uint32_t)(mine_of >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)mine_of, 0));
+      if (at < a.top)
+        __hip_atomic_store(&out_keys[piece * a.top + at], in[0] ? key : 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     uint32_t* const counter = (uint32_t*)a.scratch + row * kCounterStep;
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wavefront's stores are there
