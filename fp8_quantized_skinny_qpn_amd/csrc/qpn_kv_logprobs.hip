@@ -128,7 +128,6 @@ __device__ __forceinline__ uint32_t bound_of(const uint32_t (&x)[N], int top, in
     low = min(low, x[i] - 1u);  // (0: the largest)
   }
   if (reach < top) return 0;
-  if (reach == 0) return 0;
   uint32_t t = wave_min(low) + 1;
   const uint32_t most = wave_max(high);
 #pragma unroll 1
@@ -218,14 +217,20 @@ __device__ __forceinline__ uint64_t gathered(const uint64_t (&key)[N], int top, 
   return lane < list.count ? room[lane] : 0;
 }
 
-// A key's place among the wavefront's, the largest first (they are all different; 0: none).
-__device__ __forceinline__ int rank_of(uint64_t key) {
+// A key's place among the wavefront's, the largest first (they are all different, in the first
+// lanes; 0: none).  room: LDS for kLanes keys.
+__device__ __forceinline__ int rank_of(uint64_t key, uint64_t* room) {
+  room[threadIdx.x & 63] = key;
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  const int count = __popcll(__ballot(key != 0));
   int rank = 0;
-  for (uint64_t left = __ballot(key != 0); left; left &= left - 1) {
-    const int i = __ffsll((unsigned long long)left) - 1;
-    const uint64_t other = (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(key >> 32), i) << 32 |
-                           (uint32_t)__builtin_amdgcn_readlane((int)key, i);
-    rank += other > key;
+#pragma unroll 1
+  for (int i = 0; i < count; i += 8) {
+    uint64_t other[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) other[j] = room[i + j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) rank += other[j] > key;
   }
   return rank;
 }
@@ -505,7 +510,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
   if constexpr (TOP) {
     const int found = __popcll(__ballot(key != 0));
     // (there are `top` of them, unless some logits are NaN; then the lanes behind fill the row)
-    const int rank = key ? rank_of(key) : lane;
+    const int place = rank_of(key, list.keys), rank = key ? place : lane;
     if (rank < a.top && (key || lane >= found)) {
       const bool none = bad || !key;
       const double zi = value_of((uint32_t)(key >> 32));
