@@ -406,7 +406,7 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
   }
 
   // the workgroup's wavefronts, by the first one
-  mine = wave_joined(mine, c);
+  mine.s = wave_sum(mine.s), mine.u = wave_sum(mine.u);  // (a wavefront has one maximum)
   if (lane == 0) s_sums[wave] = mine;
   if constexpr (TOP) {  // (in any order: the keys are all different)
     if (list.count > kMaxTop) list.cut(a.top);
