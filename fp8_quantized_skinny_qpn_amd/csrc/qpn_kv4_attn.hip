@@ -247,6 +247,17 @@ __device__ __forceinline__ float half_max(const float4v (&x)[2][RT], int rt) {
 // ---------------------------------------------------------------------------
 // Few rows: each wavefront takes pages of its own, all rows of the segment, straight
 // into registers; the workgroup's wavefronts are joined through LDS at the end.
+//
+// Bound by the bytes of the cache (4.5 bits a value), and close behind by instructions: of
+// 8 rows of 5 query heads a page costs a wavefront 102 matrix instructions, 48
+// exponentials and the conversion of 16384 codes, on a SIMD that two wavefronts share.  Half a page
+// at a time, 32 tokens, a k-step of the second product: scores and weights of a whole page
+// leave no registers for the next page's codes, which are loaded as soon as this page's last
+// are converted (104 us by whole pages, 87 by halves).  Codes through a ring in LDS, which
+// would have more of them on their way, lose (92): what LDS gives back has to be waited for
+// again.  8 rows over 244608 tokens, 40 + 8 heads of 128: 76-81 us, 282 MB at 3.5-3.7 TB/s; 64
+// requests of up to 12000 tokens (10 + 2 heads, 102 MB) 40; 8 rows over 5001 tokens 12.4; one
+// row over 300 8.6.
 // ---------------------------------------------------------------------------
 template <int DIM, int RT>
 struct FewLds {
@@ -461,6 +472,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void attention4_few_kernel(Attentio
 // A operands.  The scores of the next page are computed beside the weights of this
 // one, so that the matrix and the vector units work at the same time; keys are
 // therefore one page ahead of values.  Two buffers of each, one barrier a page.
+//
+// Bound by the matrix and the vector units together: of a page, a SIMD's two wavefronts have 128
+// matrix instructions of 16 cycles, and about as many cycles of exponentials, maxima and
+// conversions each; LDS hands out its 256 KB a page in 2048 cycles as well.  The codes of the next
+// page are loaded a step ahead, 1 KiB of them a wavefront (of 128 dimensions: four have keys,
+// four values).  256 rows over 16500 tokens, 40 + 8 heads of 128: 98 us and 9 of the join, 107 on
+// a stream: 800 TFLOP/s.
 // ---------------------------------------------------------------------------
 template <int DIM>
 struct ManyLds {

@@ -36,6 +36,11 @@ struct Place {
 // the slots behind its row's), and every code goes to a byte that no other row writes.
 // A wavefront takes a row and HPW = 64 / LPH KV heads, eight dimensions a lane; two
 // neighbouring lanes are a group.
+//
+// One row is bound by a chain (slot, row, 64-bit angles, norms and codes, stores) behind a
+// launch: 4.8 us with 40 + 8 heads of 128.  1024 rows, 30 MB, take 13.4 where a copy of the bytes
+// takes 6.2: the 64-bit angles of a row are found by its two wavefronts of KV heads and each
+// of those of queries.
 // ---------------------------------------------------------------------------
 
 // Eight values of a group as E2M1 codes, element e at bits 4 e, and the group's scale
@@ -167,7 +172,8 @@ hipError_t launch_append4(const RopeAppend4Args& a) {
 // ---------------------------------------------------------------------------
 // Reading back: a lane takes eight dimensions of a token and head, a workgroup
 // neighbouring rows of one head, so that the lines of a page that neighbouring tokens
-// share are read together and rows are written in whole lines.
+// share are read together and rows are written in whole lines.  Bound by what it writes:
+// 32768 tokens of 8 heads of 128, 172 MB, in 40 us, 4.3 TB/s (a large copy: 4.9).
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ half8 scaled(const float x[8], float unit) {
   half8 y;

@@ -19,6 +19,13 @@
 // bisections of the values and then of the indices of the last one's equals, when it is
 // long and at the end.  Wavefronts of a workgroup and then the pieces of a row are
 // joined in the same way, by the last one of a row to arrive, which also sorts.
+//
+// Rows of 151936 tokens: one, top 20, in 13.0 us, eight, top 5, in 11.0: a chain of
+// the launch, a tile, the joins within a workgroup and between ten of them, each step of
+// which waits for the one before (an instruction of the joins is run once and by few
+// wavefronts).  256 rows, top 20, in 27.6, 78 MB at 2.8 TB/s: a workgroup a CU, whose
+// start and joins nothing hides.  Of the value's bits only those are bisected in which the least
+// and the largest differ (with all 16, and wavefronts reduced through LDS: 16.9, 14.6 and 30.8).
 #include <type_traits>
 
 #include "qpn_common.h"
