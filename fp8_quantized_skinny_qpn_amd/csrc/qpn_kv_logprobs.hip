@@ -271,8 +271,9 @@ __global__ __launch_bounds__(kThreads) void logprobs_kernel(LogprobsArgs a, int 
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int row = (int)(blockIdx.x / (uint32_t)pieces), piece = (int)(blockIdx.x % (uint32_t)pieces);
   const uint16_t* const z = a.logits + row * a.logits_stride;
-  // (as good as any larger one: two logits differ by 2^-24 at least)
-  const float c = (float)(fmin(a.inv_temperature, 1e30) * 1.4426950408889634074);
+  // (as good as any larger or smaller one: two logits differ by 2^-24 at least and, but for -inf, by
+  // 2^17 at most; not zero, so that -inf stays what it is)
+  const float c = (float)(fmin(fmax(a.inv_temperature, 1e-30), 1e30) * 1.4426950408889634074);
 
   // tiles start at multiples of 16 bytes: the first one up to seven tokens before the row
   const int before = (int)(((uintptr_t)z >> 1) & 7);

@@ -38,6 +38,8 @@ def check(kv, z, tokens, top, temperature=1.0, zd=None, **more):
     assert np.array_equal(ids, rids)
     d = 46 * 2.0 ** -22 * np.minimum(np.maximum(s1, 0), 1) + 2.0 ** -50
     for a, b, e in ((lp, rl, d), (h, rh, d + 46 * 2.0 ** -22 * np.abs(rh)), (lps, rlps, d[:, None])):
+        # FP32 rounds what is 2^128 - 2^103 or more (its largest number and half a step) to infinity
+        b = np.where(np.abs(b) >= 2.0 ** 128 - 2.0 ** 103, np.copysign(np.inf, b), b)
         assert np.array_equal(np.isnan(a), np.isnan(b)) and np.array_equal(np.isinf(a), np.isinf(b))
         ok = np.isfinite(b)
         assert np.array_equal(a[np.isinf(b)], b[np.isinf(b)])
@@ -63,6 +65,16 @@ def test_temperatures(kv, temperature):
     rng = np.random.default_rng(2)
     z = (4 * rng.standard_normal((6, 3001))).astype(np.float16)
     check(kv, z, z.argsort(1)[:, -2], 20, temperature)
+
+
+@pytest.mark.parametrize("temperature", [1e10, 1e40, 1e300, 1e-10, 1e-40])
+def test_far_temperatures_with_masked_tokens(kv, temperature):
+    rng = np.random.default_rng(9)
+    z = (3 * rng.standard_normal((4, 3000))).astype(np.float16)
+    z[:, ::3] = -np.inf
+    z[1, :2990] = -np.inf
+    z[2] = np.float16(65504) * rng.choice([-1, 1], 3000)
+    check(kv, z, [1, 2995, 5, 0], 8, temperature)
 
 
 def test_likely_tokens_keep_their_precision(kv):
