@@ -39,8 +39,9 @@ struct Place {
 //
 // One row is bound by a chain (slot, row, 64-bit angles, norms and codes, stores) behind a
 // launch: 4.8 us with 40 + 8 heads of 128.  1024 rows, 30 MB, take 13.4 where a copy of the bytes
-// takes 6.2: the 64-bit angles of a row are found by its two wavefronts of KV heads and each
-// of those of queries.
+// takes 6.2: 9.0 with the queries alone, 8.8 with keys and values alone, of which the vector
+// units' work adds up.  (A row's angles are found by each of its wavefronts: five of queries
+// instead of two 13.9, ten 16.1.)
 // ---------------------------------------------------------------------------
 
 // Eight values of a group as E2M1 codes, element e at bits 4 e, and the group's scale

@@ -435,6 +435,32 @@ def test_attention_bad_pages_many_rows(kv, rows, page):
     assert np.isnan(y[first:]).all() and np.array_equal(y[:first], clean[:first])
 
 
+@pytest.mark.parametrize("rows", [3, 90])
+def test_attention_long_tables_in_one_piece(kv, rows):
+    # page numbers are loaded 64 at a time: bad ones around the ends of those, with segments whole (no scratch)
+    tokens = 64 * 133 + 5
+    c = AttnCase4(kv, [(rows, tokens)], 4, 1, 64, 23)
+    c.check(c.run())
+    cache, none = c.device(), torch.zeros(0, dtype=torch.uint8, device="cuda")
+    args = dev(c.q.reshape(rows, -1)), i32(c.row_start), i32(c.seq)
+    y = host(kv.attention(cache, *args, i32(c.table), rows, scratch_=none)).reshape(c.q.shape)
+    c.check(y.astype(np.float64))
+    for page in (0, 1, 62, 63, 64, 65, 127, 128, 132):
+        bad = c.table.copy()
+        bad[0, page] = -1
+        got = host(kv.attention(cache, *args, i32(bad), rows, scratch_=none))
+        sees = np.arange(tokens - rows, tokens) >= 64 * page     # (the last page is behind the first rows)
+        assert np.isnan(got[sees]).all() and np.isfinite(got[~sees]).all(), page
+        # in a window: NaN in the rows for which the page's last token is not behind it, and the others as if
+        # the page were there
+        window = 64 * (132 - page)
+        if window > 0:
+            good, got = (host(kv.attention(cache, *args, i32(t), rows, window=window, scratch_=none))
+                         for t in (c.table, bad))
+            sees = np.arange(tokens - rows, tokens) - window < 64 * page + 63
+            assert np.isnan(got[sees]).all() and np.array_equal(got[~sees], good[~sees]), page
+
+
 @pytest.mark.parametrize("dim,hq,hk", [(64, 4, 2), (128, 2, 2), (256, 8, 1)])
 @pytest.mark.parametrize("rows,tokens", [(8, 6), (100, 90), (200, 256), (200, 300)])
 def test_attention_more_rows_than_the_table_has_places(kv, dim, hq, hk, rows, tokens):
