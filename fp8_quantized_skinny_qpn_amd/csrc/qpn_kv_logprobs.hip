@@ -30,6 +30,7 @@
 
 #include "qpn_common.h"
 #include "qpn_kv_internal.h"
+#include "qpn_kv_order.h"
 
 namespace qpn {
 
@@ -47,7 +48,7 @@ constexpr int kWanted = 256;                      // workgroups wanted: one a CU
 constexpr int kCounterStep = 16;                  // 32-bit words between the rows' counters
 static_assert((size_t)kWanted * kCounterStep * 4 <= kKvZeroedBytes, "a counter per row of a call with cut rows");
 constexpr float kLowest = -65504.0f;
-constexpr uint32_t kOrderedLowest = 0x03FFu;      // ordered(-inf)
+constexpr uint32_t kOrderedLowest = ordered_bits(0xFC00u);  // -inf's
 
 struct Sums {
   float m;      // the largest logit (at least kLowest)
@@ -60,21 +61,12 @@ struct Piece {
   float m, pad;
 };
 
-// Ascending in the value: the bits of an FP16 number (no NaN; -0 as 0).
-__device__ __forceinline__ uint32_t ordered_bits(uint32_t b) {
-  b = b == 0x8000u ? 0u : b;
-  return b & 0x8000u ? b ^ 0xFFFFu : b | 0x8000u;
-}
 __device__ __forceinline__ uint32_t ordered(float z) {
   return ordered_bits(__builtin_bit_cast(uint16_t, (_Float16)z));
 }
 __device__ __forceinline__ float value_of(uint32_t o) {
-  return (float)__builtin_bit_cast(_Float16, (uint16_t)(o & 0x8000u ? o ^ 0x8000u : o ^ 0xFFFFu));
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)bits_of_ordered(o));
 }
-__device__ __forceinline__ uint64_t key_of(uint32_t order, uint32_t index) {
-  return (uint64_t)order << 32 | (0xFFFFFFFFu - index);
-}
-__device__ __forceinline__ int index_of(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
 // x of another lane by a data-parallel move, and reductions by them: within 16 lanes (quad_perm
 // 1 0 3 2 and 2 3 0 1, mirrored within 8 and 16), then of the four rows' first lanes.  The
@@ -121,8 +113,8 @@ __device__ __forceinline__ double wave_sum(double x) {
   return wave_reduced(x, [](double a, double b) { return a + b; });
 }
 
-// The largest t for which at least `top` of the wavefront's values (N a lane; those of lanes
-// without one: 0) are t or more, and how many are; 0 and their number when there are fewer.
+// The largest t for which at least `top` of the wavefront's values (N a lane, from 1 on; those of
+// lanes without one: 0) are t or more, and how many are; 0 and their number when there are fewer.
 // Bisected between the least and the largest of them.
 template <int N>
 __device__ __forceinline__ uint32_t bound_of(const uint32_t (&x)[N], int top, int& reach) {
@@ -185,7 +177,9 @@ struct List {
     count += __popcll(mask);
   }
 
-  // Cuts the list to its `top` largest keys.
+  // Cuts the list, of more than `top` keys, to its `top` largest.  (Just as many, whatever the logits
+  // were: every key counts in bound_of, as ordered_bits is never 0, and no two are equal.  The room
+  // behind kListMax is for what one add() may bring after it.)
   __device__ __forceinline__ void cut(int top) {
     constexpr int N = kListRoom / kLanes;
     const int lane = threadIdx.x & 63;

@@ -161,3 +161,25 @@ def test_scratch_outputs_and_graphs(kv):
         torch.cuda.synchronize()
         for got, w in ((out, want[i % 3]), (again, want[i % 3]), (eager, want[(i + 1) % 3])):
             assert all(np.array_equal(host(a), b) for a, b in zip(got, w))
+
+
+@pytest.mark.parametrize("n,rows", [(700, 9), (5000, 9), (40001, 9), (40001, 300)])   # a tile, a piece, several pieces, one
+@pytest.mark.parametrize("bits", [0xFFFF, 0xFFFE, 0xFE00, 0xFC01, 0x7FFF, 0x7E00, 0x7C01])
+def test_nan_of_any_bits(kv, n, rows, bits):
+    # whole rows, tiles, the ends of rows and single tokens of it, among numbers and among masked ones; every other row
+    # holds numbers alone
+    rng = np.random.default_rng(n)
+    z = (3 * rng.standard_normal((rows, n))).astype(np.float16)
+    u = z.view(np.uint16)
+    u[1] = bits
+    u[3, n // 2:n // 2 + 1024] = bits
+    u[5] = 0xFC00
+    u[5, ::2] = bits
+    u[7] = 0xFC00
+    u[7, [0, n - 1]] = 0x3C00, bits
+    z[8, 3:] = -np.inf
+    if rows > 100:
+        u[100:164:2, ::3] = bits
+    tokens = rng.integers(0, n, rows)
+    for top in (0, 1, 20, 32):
+        check(kv, z, tokens, top)
