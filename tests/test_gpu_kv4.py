@@ -694,3 +694,60 @@ def test_calls_beside_each_other(kv):
         torch.cuda.synchronize()
         for out in (eager, *(o[i:i + 5] for _, o in graphs for i in (0, 5))):
             same(out)
+
+
+# ---------------------------------------------------------------- calls that a server makes and the above leave out
+
+@pytest.mark.parametrize("rows", [3, 70])
+def test_attention_queries_that_are_no_numbers(kv, rows):
+    # a NaN query has no scores; an infinite one's are infinite, or NaN where the key's code is zero: NaN throughout the
+    # row in either case, and nothing in the others
+    c = AttnCase4(kv, [(rows, 100)], 4, 1, 64, 10)
+    clean = c.run()
+    c.q[1, 2, 5] = np.inf
+    c.q[2, 0, 0] = np.nan
+    c.q[0, 3, 63] = -np.inf
+    y = c.run()
+    hit = np.zeros(y.shape, bool)
+    hit[1, 2] = hit[2, 0] = hit[0, 3] = True
+    assert np.array_equal(np.isnan(y), hit)
+    assert np.array_equal(y[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("dim,hq,hk", [(128, 40, 8), (64, 40, 8), (256, 20, 4), (128, 10, 2)])
+@pytest.mark.parametrize("width", [1024, 1025, 4096])
+@pytest.mark.parametrize("lens", [[(8, 300)], [(8, 5001)], [(1, 700)], [(70, 900)], [(8, 200), (3, 900), (0, 70), (5, 64)]])
+def test_attention_tables_wider_than_any_request(kv, dim, hq, hk, width, lens):
+    # a server's tables are as wide as its longest context, and what lies behind a request's pages is anything; the
+    # width decides whether the row tiles of a KV head are taken together
+    c = AttnCase4(kv, lens, hq, hk, dim, 31)
+    pages = c.codes.shape[1]
+    wide = np.random.default_rng(4).choice([-7, 0, pages - 1, pages, 2 ** 31 - 1, -2 ** 31], (len(lens), width))
+    wide[:, :c.width][c.table >= 0] = c.table[c.table >= 0]
+    c.table = wide
+    q = dev(c.q.reshape(c.q.shape[0], -1))
+    for window in (0, 100):
+        log(f"attention {lens} heads {hq}/{hk} dim {dim} table {width} window {window}")
+        y = kv.attention(c.device(), q, i32(c.row_start), i32(c.seq), i32(c.table), max(r for r, _ in lens), window=window)
+        c.table = np.clip(wide, 0, pages - 1)                      # (for the reference, which looks at what is seen alone)
+        c.check(host(y).reshape(c.q.shape).astype(np.float64), window)
+        c.table = wide
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_attention_many_rows_far_offsets(kv, dim):
+    # codes of over 2^32 bytes a side, a prompt block over the last pages, with a NaN group that its rows see in part
+    pages, hk = 70000 * 256 // dim, 8
+    small = AttnCase4(kv, [(150, 700)], 16, hk, dim, 12, extra_pages=0)
+    n = small.codes.shape[1]
+    small.scale[1, small.table[0, 9], 3, 20, 1] = 0x7F
+    cache, part = kv.KvCache4.empty(pages, hk, dim), small.device()
+    for name in ("k", "v", "k_scale", "v_scale"):
+        getattr(cache, name).view(torch.uint8)[pages - n:] = getattr(part, name).view(torch.uint8)
+    cache.k_unit, cache.v_unit = part.k_unit, part.v_unit
+    clean = small.run()
+    hit = np.zeros(clean.shape, bool)
+    hit[9 * PAGE + 20 - 550:, 6:8, 16:32] = True                   # rows from the group's own token on
+    assert np.array_equal(np.isnan(clean), hit)
+    small.table = np.where(small.table >= 0, small.table + pages - n, small.table)
+    assert np.array_equal(small.run(cache), clean, equal_nan=True)

@@ -183,3 +183,30 @@ def test_nan_of_any_bits(kv, n, rows, bits):
     tokens = rng.integers(0, n, rows)
     for top in (0, 1, 20, 32):
         check(kv, z, tokens, top)
+
+
+@pytest.mark.parametrize("rows,n", [(1, 151936), (9, 20011), (300, 9001)])
+def test_rows_of_few_values(kv, rows, n):
+    # what a grammar leaves: fewer tokens than are asked for, the rest masked; and rows of a few different values
+    rng = np.random.default_rng(rows)
+    z = np.full((rows, n), -np.inf, np.float16)
+    for r in range(rows):
+        if r % 3 == 2:
+            z[r] = rng.integers(-1, 2, n)
+        else:
+            at = rng.choice(n, 3 + 30 * (r % 3), replace=False)
+            z[r, at] = rng.standard_normal(len(at))
+    for top in (1, 20, 32):
+        check(kv, z, rng.integers(0, n, rows), top)
+
+
+def test_far_rows(kv):
+    # rows more than 2^32 bytes behind the first
+    rows, n, stride = 2060, 1000, 1 << 20
+    rng = np.random.default_rng(8)
+    z = (3 * rng.standard_normal((rows, n))).astype(np.float16)
+    flat = torch.empty(rows * stride, dtype=torch.float16, device="cuda")
+    wide = flat.view(rows, stride)[:, :n]
+    wide.copy_(dev(z))
+    assert (rows - 1) * stride * 2 > 2 ** 32
+    check(kv, z, rng.integers(0, n, rows), 5, zd=wide)
