@@ -61,7 +61,7 @@ __device__ __forceinline__ Codes quantise(const double x[8], double unit) {
     amax = fmax(amax, a);
   }
   amax = fmax(amax, moved<0xB1>(amax));
-  finite &= __builtin_amdgcn_mov_dpp((int)finite, 0xB1, 0xF, 0xF, false) != 0;
+  finite &= moved<0xB1>((int)finite) != 0;
   if (!finite) return {0u, 0x7Fu};
   const uint32_t scale = e4m3_code(amax / (6.0 * unit));
   const double step = e4m3_value(scale) * unit;

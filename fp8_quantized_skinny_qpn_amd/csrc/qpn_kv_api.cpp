@@ -79,15 +79,15 @@ int rope_append(Launch launch, const Cache* cache, const uint16_t* qkv, int64_t 
     return QPN_ERR_ALIGN;
   rc = device_status();
   if (rc != QPN_OK) return rc;
-  return status_of(launch({cache_of(cache), qkv, qkv_stride, rows, q_heads, q_weight, k_weight, eps,
-                                       inv_freq, rot, interleaved != 0, positions, slots, q_out, q_stride, stream}));
+  return status_of(launch({cache_of(cache), qkv, qkv_stride, rows, q_heads, q_weight, k_weight, eps, inv_freq, rot,
+                           interleaved != 0, positions, slots, q_out, q_stride, stream}));
 }
 
 template <typename Cache, typename Launch>
 int attention(Launch launch, const Cache* cache, const uint16_t* q, int64_t q_stride, uint16_t* y, int64_t y_stride,
-                     int q_heads, int rows, int requests, int max_rows, const int32_t* row_start,
-                     const int32_t* seq_lens, const int32_t* table, int64_t table_stride, int table_width,
-                     float scale, int window, void* scratch, size_t scratch_bytes, void* stream) {
+              int q_heads, int rows, int requests, int max_rows, const int32_t* row_start, const int32_t* seq_lens,
+              const int32_t* table, int64_t table_stride, int table_width, float scale, int window, void* scratch,
+              size_t scratch_bytes, void* stream) {
   int rc = cache_check(cache);
   if (rc != QPN_OK) return rc;
   if (rows < 0 || rows > kKvMaxRows || requests < 0 || requests > kKvMaxRequests || max_rows < 0 ||
@@ -106,9 +106,8 @@ int attention(Launch launch, const Cache* cache, const uint16_t* q, int64_t q_st
   if (!scratch) scratch_bytes = 0;
   rc = device_status();
   if (rc != QPN_OK) return rc;
-  return status_of(launch({cache_of(cache), q, q_stride, y, y_stride, q_heads, rows, requests, max_rows,
-                                     row_start, seq_lens, table, table_stride, table_width, scale, window, scratch,
-                                     scratch_bytes, stream}));
+  return status_of(launch({cache_of(cache), q, q_stride, y, y_stride, q_heads, rows, requests, max_rows, row_start,
+                           seq_lens, table, table_stride, table_width, scale, window, scratch, scratch_bytes, stream}));
 }
 
 }  // namespace
@@ -142,8 +141,8 @@ int qpn_kv_rope_append(const qpn_kv_cache* cache, const uint16_t* qkv, int64_t q
                        const uint16_t* q_weight, const uint16_t* k_weight, double eps, const float* inv_freq,
                        int rot, int interleaved, const int32_t* positions, const int32_t* slots, uint16_t* q_out,
                        int64_t q_stride, void* stream) {
-  return rope_append(launch_rope_append, cache, qkv, qkv_stride, rows, q_heads, q_weight, k_weight, eps, inv_freq, rot, interleaved, positions,
-                     slots, q_out, q_stride, stream);
+  return rope_append(launch_rope_append, cache, qkv, qkv_stride, rows, q_heads, q_weight, k_weight, eps,
+                     inv_freq, rot, interleaved, positions, slots, q_out, q_stride, stream);
 }
 
 size_t qpn_kv_attention_scratch_bytes(int requests, int max_rows, int q_heads, int heads, int dim,
@@ -158,16 +157,16 @@ int qpn_kv_attention(const qpn_kv_cache* cache, const uint16_t* q, int64_t q_str
                      int q_heads, int rows, int requests, int max_rows, const int32_t* row_start,
                      const int32_t* seq_lens, const int32_t* table, int64_t table_stride, int table_width,
                      float scale, int window, void* scratch, size_t scratch_bytes, void* stream) {
-  return attention(launch_attention, cache, q, q_stride, y, y_stride, q_heads, rows, requests, max_rows, row_start, seq_lens,
-                   table, table_stride, table_width, scale, window, scratch, scratch_bytes, stream);
+  return attention(launch_attention, cache, q, q_stride, y, y_stride, q_heads, rows, requests, max_rows, row_start,
+                   seq_lens, table, table_stride, table_width, scale, window, scratch, scratch_bytes, stream);
 }
 
 int qpn_kv4_rope_append(const qpn_kv4_cache* cache, const uint16_t* qkv, int64_t qkv_stride, int rows, int q_heads,
-                       const uint16_t* q_weight, const uint16_t* k_weight, double eps, const float* inv_freq,
-                       int rot, int interleaved, const int32_t* positions, const int32_t* slots, uint16_t* q_out,
-                       int64_t q_stride, void* stream) {
-  return rope_append(launch_rope_append4, cache, qkv, qkv_stride, rows, q_heads, q_weight, k_weight, eps, inv_freq, rot, interleaved, positions,
-                     slots, q_out, q_stride, stream);
+                        const uint16_t* q_weight, const uint16_t* k_weight, double eps, const float* inv_freq,
+                        int rot, int interleaved, const int32_t* positions, const int32_t* slots, uint16_t* q_out,
+                        int64_t q_stride, void* stream) {
+  return rope_append(launch_rope_append4, cache, qkv, qkv_stride, rows, q_heads, q_weight, k_weight, eps,
+                     inv_freq, rot, interleaved, positions, slots, q_out, q_stride, stream);
 }
 
 int qpn_kv4_read(const qpn_kv4_cache* cache, const int32_t* slots, int rows, uint16_t* k_out, int64_t k_stride,
@@ -188,7 +187,7 @@ int qpn_kv4_read(const qpn_kv4_cache* cache, const int32_t* slots, int rows, uin
 }
 
 size_t qpn_kv4_attention_scratch_bytes(int requests, int max_rows, int q_heads, int heads, int dim,
-                                      int table_width) {
+                                       int table_width) {
   if (requests < 0 || requests > kKvMaxRequests || max_rows < 0 || max_rows > kKvMaxRows ||
       !heads_ok(q_heads, heads) || !dim_ok(dim) || table_width < 0 || table_width > kKvMaxPages)
     return (size_t)-1;
@@ -196,11 +195,11 @@ size_t qpn_kv4_attention_scratch_bytes(int requests, int max_rows, int q_heads, 
 }
 
 int qpn_kv4_attention(const qpn_kv4_cache* cache, const uint16_t* q, int64_t q_stride, uint16_t* y, int64_t y_stride,
-                     int q_heads, int rows, int requests, int max_rows, const int32_t* row_start,
-                     const int32_t* seq_lens, const int32_t* table, int64_t table_stride, int table_width,
-                     float scale, int window, void* scratch, size_t scratch_bytes, void* stream) {
-  return attention(launch_attention4, cache, q, q_stride, y, y_stride, q_heads, rows, requests, max_rows, row_start, seq_lens,
-                   table, table_stride, table_width, scale, window, scratch, scratch_bytes, stream);
+                      int q_heads, int rows, int requests, int max_rows, const int32_t* row_start,
+                      const int32_t* seq_lens, const int32_t* table, int64_t table_stride, int table_width,
+                      float scale, int window, void* scratch, size_t scratch_bytes, void* stream) {
+  return attention(launch_attention4, cache, q, q_stride, y, y_stride, q_heads, rows, requests, max_rows, row_start,
+                   seq_lens, table, table_stride, table_width, scale, window, scratch, scratch_bytes, stream);
 }
 
 size_t qpn_kv_verify_scratch_bytes(int rows, int requests, int64_t n) {

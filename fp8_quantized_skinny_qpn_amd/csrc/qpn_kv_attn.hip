@@ -31,6 +31,12 @@ namespace qpn {
 
 namespace {
 
+// A load of 16 bytes a lane into LDS: lane i's go to lds + 16 i.
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)lds)), "v"(offset), "s"(base)
+               : "memory", "m0");
+}
+
 // wavefronts of a workgroup, few rows: one per 16 dimensions up to eight
 constexpr int few_waves(int dim) { return dim == 64 ? 4 : 8; }
 

@@ -14,6 +14,7 @@
 
 #include "qpn_common.h"
 #include "qpn_kv_internal.h"
+#include "qpn_kv_lanes.h"
 
 namespace qpn {
 
@@ -107,15 +108,8 @@ __device__ __forceinline__ Req request_of(const A& a, const AttnLaunch& l, int r
   return q;
 }
 
-// The sum over the wavefront, in every lane: within 16 lanes by data-parallel moves (quad_perm
-// 1 0 3 2 and 2 3 0 1, mirrored within 8 and 16), then between the four rows.
 __device__ __forceinline__ int wave_sum(int x) {
-  x += __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, false);
-  x += __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, false);
-  x += __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, false);
-  x += __builtin_amdgcn_mov_dpp(x, 0x140, 0xF, 0xF, false);
-  return (__builtin_amdgcn_readlane(x, 0) + __builtin_amdgcn_readlane(x, 16)) +
-         (__builtin_amdgcn_readlane(x, 32) + __builtin_amdgcn_readlane(x, 48));
+  return wave_reduced(x, [](int a, int b) { return a + b; });
 }
 
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
@@ -499,12 +493,6 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
-}
-
-// A load of 16 bytes a lane into LDS: lane i's go to lds + 16 i.
-__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uniform((int)lds)), "v"(offset), "s"(base)
-               : "memory", "m0");
 }
 
 template <int RT, typename A>

@@ -8,6 +8,7 @@
 
 #include "qpn_common.h"
 #include "qpn_kv_internal.h"
+#include "qpn_kv_lanes.h"
 
 namespace qpn {
 
@@ -76,19 +77,6 @@ __device__ __forceinline__ half8 load_half8(const uint16_t* p) {
   return *reinterpret_cast<const half8*>(p);
 }
 
-// x of another lane by a data-parallel move: within four lanes (quad_perm 1 0 3 2
-// and 2 3 0 1), mirrored within eight, within sixteen.
-template <int CTRL>
-__device__ __forceinline__ float moved(float x) {
-  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), CTRL, 0xF, 0xF, false));
-}
-template <int CTRL>
-__device__ __forceinline__ double moved(double x) {
-  const uint64_t b = (uint64_t)__double_as_longlong(x);
-  const uint32_t lo = (uint32_t)__builtin_amdgcn_mov_dpp((int)b, CTRL, 0xF, 0xF, false);
-  const uint32_t hi = (uint32_t)__builtin_amdgcn_mov_dpp((int)(b >> 32), CTRL, 0xF, 0xF, false);
-  return __longlong_as_double((long long)(((uint64_t)hi << 32) | lo));
-}
 // Over LANES (8 to 64) neighbouring lanes, in every one of them.
 template <int LANES, typename T>
 __device__ __forceinline__ T lanes_sum(T x) {
