@@ -33,11 +33,15 @@ struct KindOf<Attention4Args> {
   static constexpr int many_tiles(int dim) { return dim == 256 ? 1 : 2; }
   // Several tiles of a KV head in one workgroup decode its codes once, but leave as many times
   // the sums to join: with few segments, up to some length, a workgroup a tile is the faster
-  // one.  8 rows of 40 + 8 heads (three tiles) over 1000 / 5001 / 32000 / 64000 / 131001 tokens:
-  // together 15.6 / 19.5 / 30.5 / 38.3 / 56.8 us, apart 11.3 / 13.1 / 25.8 / 38.2 / 68.4; 3
-  // requests of them over up to 4000 21.0 and 21.1, 4 over up to 8000 27.5 and 28.5.  Where no
-  // segment is cut, while a workgroup each finds a CU: 10 requests over up to 500 tokens 15.3
-  // and 12.3, 16 of them 15.4 and 23.2.
+  // one.  8 rows of 40 + 8 heads of 128 (three tiles) over 300 / 1000 / 5001 / 32000 / 64000
+  // tokens: together 12.7 / 15.5 / 19.3 / 29.0 / 35.7 us, apart 8.8 / 11.4 / 12.7 / 24.2 / 35.4
+  // (131001: 56.8 and 68.4); of 64 dimensions together 10.1 / 12.6 / 15.2 / 23.0 / 27.2, apart
+  // 8.9 / 9.8 / 10.9 / 18.6 / 25.5; of 256 there is one tile.  3 requests of them over up to 4000
+  // 20.7 and 19.9, 4 over up to 8000 27.5 and 28.5.  Where no segment is cut, while a workgroup
+  // each finds a CU: 10 requests over up to 500 tokens 14.7 and 9.9, 16 of them 14.5 and 23.2.
+  // What the host knows of the lengths is the table's width (the longest request it has room
+  // for), and that decides: in a table of more than 24576 pages over tiles x groups (1024 for
+  // these heads) short requests take the tiles together, 5001 tokens 19.3 us.
   static constexpr bool apart(int64_t tiles, int64_t groups, int64_t pages) {
     return tiles * groups <= (pages <= kMinPiecePages ? 256 : 80) && tiles * groups * pages <= 24576;
   }
@@ -248,15 +252,16 @@ __device__ __forceinline__ float half_max(const float4v (&x)[2][RT], int rt) {
 // Few rows: each wavefront takes pages of its own, all rows of the segment, straight
 // into registers; the workgroup's wavefronts are joined through LDS at the end.
 //
-// Bound by the bytes of the cache (4.5 bits a value), and close behind by instructions: of
-// 8 rows of 5 query heads a page costs a wavefront 102 matrix instructions, 48
-// exponentials and the conversion of 16384 codes, on a SIMD that two wavefronts share.  Half a page
+// Bound by instructions and the bytes of the cache (4.5 bits a value) alike: of 8 rows of 5 query
+// heads a page costs a wavefront 102 matrix instructions, 48 exponentials and the conversion of
+// 16384 codes, on a SIMD that two wavefronts share; over 244608 tokens vector instructions are
+// issued 66% of the time and the matrix unit is busy 35%, at 3.4 TB/s.  Half a page
 // at a time, 32 tokens, a k-step of the second product: scores and weights of a whole page
 // leave no registers for the next page's codes, which are loaded as soon as this page's last
 // are converted (104 us by whole pages, 87 by halves).  Codes through a ring in LDS, which
 // would have more of them on their way, lose (92): what LDS gives back has to be waited for
-// again.  8 rows over 244608 tokens, 40 + 8 heads of 128: 76-81 us, 282 MB at 3.5-3.7 TB/s; 64
-// requests of up to 12000 tokens (10 + 2 heads, 102 MB) 40; 8 rows over 5001 tokens 12.4; one
+// again.  Calls one behind another: 8 rows over 244608 tokens, 40 + 8 heads of 128, 282 MB, 82 us;
+// 64 requests of up to 12000 tokens (10 + 2 heads, 102 MB) 40; 8 rows over 5001 tokens 12.5; one
 // row over 300 8.6.
 // ---------------------------------------------------------------------------
 template <int DIM, int RT>
@@ -473,12 +478,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void attention4_few_kernel(Attentio
 // one, so that the matrix and the vector units work at the same time; keys are
 // therefore one page ahead of values.  Two buffers of each, one barrier a page.
 //
-// Bound by the matrix and the vector units together: of a page, a SIMD's two wavefronts have 128
-// matrix instructions of 16 cycles, and about as many cycles of exponentials, maxima and
-// conversions each; LDS hands out its 256 KB a page in 2048 cycles as well.  The codes of the next
-// page are loaded a step ahead, 1 KiB of them a wavefront (of 128 dimensions: four have keys,
-// four values).  256 rows over 16500 tokens, 40 + 8 heads of 128: 98 us and 9 of the join, 107 on
-// a stream: 800 TFLOP/s.
+// Bound by the matrix and the vector units, which two wavefronts a SIMD keep from waiting for one
+// another only in part: of a page's 5200 cycles the matrix unit is busy 2190 (a SIMD's two
+// wavefronts have 64 instructions of 16 cycles each for the products, and the weights' sums) and
+// vector instructions are issued in 2470; LDS is busy 1450.  The codes of the next page are loaded
+// a step ahead, 1 KiB of them a wavefront (of 128 dimensions: four have keys, four values).  256
+// rows over 16500 tokens, 40 + 8 heads of 128: 108 us for both kernels, calls one behind another
+// (796 TFLOP/s); under the profiler 102 and 9.6 for the join.
 // ---------------------------------------------------------------------------
 template <int DIM>
 struct ManyLds {

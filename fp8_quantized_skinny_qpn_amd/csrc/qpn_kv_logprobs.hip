@@ -20,12 +20,17 @@
 // long and at the end.  Wavefronts of a workgroup and then the pieces of a row are
 // joined in the same way, by the last one of a row to arrive, which also sorts.
 //
-// Rows of 151936 tokens: one, top 20, in 13.0 us, eight, top 5, in 11.0: a chain of
-// the launch, a tile, the joins within a workgroup and between ten of them, each step of
-// which waits for the one before (an instruction of the joins is run once and by few
-// wavefronts).  256 rows, top 20, in 27.6, 78 MB at 2.8 TB/s: a workgroup a CU, whose
-// start and joins nothing hides.  Of the value's bits only those are bisected in which the least
-// and the largest differ (with all 16, and wavefronts reduced through LDS: 16.9, 14.6 and 30.8).
+// Rows of 151936 tokens, calls one behind another: one, top 20, in 13.5 us, eight, top 5, in 11.1
+// (both 8.6 without alternatives): a chain of the launch, a tile, the joins within a workgroup and
+// between ten of them, each step of which waits for the one before (an instruction of the joins is
+// run once and by few wavefronts).  256 rows, top 20, in 27.9 (16.6 without), 78 MB at 2.8 TB/s: a
+// workgroup a CU; vector instructions are issued 82% of the time.  257 rows take a second turn of
+// the chip: 47.  Of the value's bits only those are bisected in which the least and the largest
+// differ (with all 16, and wavefronts reduced through LDS: 16.9, 14.6 and 30.8).
+//
+// That is of logits that spread.  A list is only cut, and `least` not raised, when tokens equal to
+// the last one that counts keep coming, so that they all go through the lists: a row with all but
+// ten tokens at -inf takes 42 us (256 rows 217), of equal logits 28 (148), of whole numbers 20 (35).
 #include <type_traits>
 
 #include "qpn_common.h"

@@ -346,7 +346,8 @@ def attention(cache: KvCache, q, row_start, seq_lens, table, max_rows: int, scal
               out=None, stream=None, scratch_=None) -> torch.Tensor:
     """Attention of the rows q [rows, q_heads * dim] over the cache through qpn_kv_attention
     (qpn_kv4_attention for a KvCache4).
-    `max_rows`: the most rows of one request (a hint).  `scale` defaults to dim ** -0.5."""
+    `max_rows`: the most rows of one request (a hint; over a KvCache4 the table's width is one of its
+    length).  `scale` defaults to dim ** -0.5."""
     d = cache.dim
     n = seq_lens.shape[0]
     shape = q.shape

@@ -213,12 +213,14 @@ QPN_API size_t qpn_kv_logprobs_scratch_bytes(int rows, int64_t n);
  * -inf, gives NaN throughout and ids of -1.
  * Exponentials are FP32, off by up to 2^-23 (1 + |x|) of themselves for exp(x); their
  * sum is FP64 and held so that a token's probability near 1 keeps a relative precision
- * of its distance from 1; results are rounded to FP32.  Deterministic but for
- * the order of a row's pieces, which is fixed too.
+ * of its distance from 1; results are rounded to FP32.  The same call on rows that lie
+ * alike (sizes, top, address modulo 16 bytes) gives the same bits; the order of the sums
+ * depends on these.
  * 0 <= rows <= 65535, 1 <= n <= 2^24, 0 <= top <= min(n, QPN_KV_MAX_TOP) (top_ids and
  * top_logprobs may be NULL when 0), inv_temperature > 0 and finite.  logits need
- * no more than their 2-byte alignment; rows at multiples of 16 bytes are as fast as
- * others but for their ends.  One kernel. */
+ * no more than their 2-byte alignment.  One kernel.  With top > 0, rows that mask all but
+ * a few tokens, or hold few different values, take up to eight times as long as rows
+ * whose logits spread. */
 QPN_API int qpn_kv_logprobs(const uint16_t *logits, int64_t logits_stride, const int32_t *tokens,
                             int rows, int64_t n, double inv_temperature, int top, float *logprob,
                             float *entropy, int32_t *top_ids, float *top_logprobs, void *scratch,

@@ -92,11 +92,14 @@ QPN_API size_t qpn_kv4_attention_scratch_bytes(int requests, int max_rows, int q
  * outside the cache, a key group whose scale is NaN, or a unit that is not positive and
  * finite gives NaN in the rows that see it; a value group whose scale is NaN gives NaN
  * in its 16 dimensions of the rows that see it.
- * Scores, weights' sums and outputs are held in FP32; keys and values enter the
- * products as code * scale, exact in FP16.  For the second product each weight, in
- * units in which a row's largest is from 1 to 2^8, is rounded to FP16: it is off by up
- * to 2^-11 of itself, or 2^-25 where it is below 2^-14 (the output's own rounding:
- * 2^-11).  Deterministic. */
+ * Scores (times log2 e), weights' sums and outputs are held in FP32: a row with a score
+ * of 2^127 or more may be NaN.  Keys and values enter the products as code * scale, exact
+ * in FP16.  For the second product each weight, in units in which a row's largest is from
+ * 1 to 2^8, is rounded to FP16: it is off by up to 2^-11 of itself, or 2^-25 where it is
+ * below 2^-14 (the output's own rounding: 2^-11).  Deterministic.
+ * table_width is also the hint of the longest request, by which the work is split: with
+ * several rows x query heads of a KV head and few requests, a table much wider than the
+ * requests need costs about half as much again. */
 QPN_API int qpn_kv4_attention(const qpn_kv4_cache *cache, const uint16_t *q, int64_t q_stride,
                               uint16_t *y, int64_t y_stride, int q_heads, int rows, int requests,
                               int max_rows, const int32_t *row_start, const int32_t *seq_lens,
